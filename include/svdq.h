@@ -340,6 +340,113 @@ SVDQ_API svdq_status svdq_linear_gelu_quantize(const uint8_t* Xq, const uint8_t*
 SVDQ_API svdq_status svdq_gelu_bf16(const uint16_t* X, int64_t n, uint16_t* Y, svdq_stream_t stream);
 
 /*
+ * 8-bit integer form of the layer (SmoothQuant W8A8; "From SmoothQuant to SVDQuant",
+ * section Smooth Quant (W8A8)): for the layers that four bits harm.
+ *
+ *     Y = Q8(X diag(s)^-1) Q8(diag(s) W) + bias
+ *
+ * Both operands are int8 codes with one float32 scale per row of X (token) and
+ * per column of W (output channel), so the sum over K is an exact integer.  The
+ * codec, each step one correctly rounded float32 operation, on a row with
+ * a = max |x_hat|:
+ *     scale = f32(a / 127),  code = rint_even(f32(x_hat * f32(127 / a)))
+ *   - a < 2^-100: scale 0 and all codes 0;
+ *   - a infinite or NaN: scale NaN and all codes 0 (the output row is NaN).
+ * Element types are given by svdq_dtype.  Shapes: K % 16 == 0, K < 131072 (the
+ * 32-bit sum cannot overflow below that), N >= 1, M >= 0 (M = 0 launches nothing;
+ * its buffer pointers may be NULL).  Row pitches (ldx, ldy) count elements; a
+ * row of X starts on 16 bytes (ldx times the element size % 16 == 0), a row of Y
+ * anywhere (ldy >= N).  Pointers are 16-byte aligned as for every call.
+ */
+typedef enum {
+    SVDQ_BF16 = 0,
+    SVDQ_FP32 = 1,
+    SVDQ_FP16 = 2
+} svdq_dtype;
+
+/*
+ * svdq_pack_weight_i8 -- offline quantization of the smoothed weight.
+ *   W_hat [in]  float32, K x N row-major (N contiguous): diag(s) W.
+ *   Wq    [out] int8, N x K: codes of W_hat^T (row n holds column n).
+ *   sw    [out] float32, N.
+ * One launch.
+ */
+SVDQ_API svdq_status svdq_pack_weight_i8(const float* W_hat, int64_t K, int64_t N, int8_t* Wq, float* sw,
+                                         svdq_stream_t stream);
+
+/*
+ * svdq_quantize_act_i8 -- per-token quantization with the smoothing fused.
+ *   X     [in]  x_type, M rows of K at pitch ldx;  x_hat = f32(X * inv_s).
+ *   inv_s [in]  float32, K, or NULL (x_hat = X).
+ *   Xq    [out] int8, M x K;  sx [out] float32, M.
+ */
+SVDQ_API svdq_status svdq_quantize_act_i8(const void* X, int x_type, int64_t ldx, int64_t M, int64_t K,
+                                          const float* inv_s, int8_t* Xq, float* sx, svdq_stream_t stream);
+
+/*
+ * svdq_linear_i8 -- int8 GEMM, scales and bias in its epilogue:
+ *   Y[m, n] = sx[m] sw[n] sum_k Xq[m, k] Wq[n, k] + bias[n]
+ * in float32 from the exact integer sum, rounded once to y_type.
+ *   Xq, sx [in] from svdq_quantize_act_i8;  Wq, sw [in] from svdq_pack_weight_i8.
+ *   bias   [in] float32, N, or NULL.
+ *   Y      [out] y_type, M rows of N at pitch ldy (columns past N are not touched).
+ */
+SVDQ_API svdq_status svdq_linear_i8(const int8_t* Xq, const float* sx, const int8_t* Wq, const float* sw,
+                                    const float* bias, void* Y, int y_type, int64_t ldy, int64_t M, int64_t N,
+                                    int64_t K, svdq_stream_t stream);
+
+/*
+ * svdq_forward_i8 -- the layer in one call: svdq_quantize_act_i8 into the
+ * workspace, then svdq_linear_i8; the same results as the two calls.
+ *   workspace [scratch] svdq_forward_i8_workspace_bytes(M, K) bytes, no initial
+ *             contents needed; calls that may overlap need workspaces of their own.
+ */
+SVDQ_API size_t svdq_forward_i8_workspace_bytes(int64_t M, int64_t K);
+SVDQ_API svdq_status svdq_forward_i8(const void* X, int x_type, int64_t ldx, const float* inv_s, const int8_t* Wq,
+                                     const float* sw, const float* bias, void* Y, int y_type, int64_t ldy, int64_t M,
+                                     int64_t N, int64_t K, void* workspace, size_t workspace_bytes,
+                                     svdq_stream_t stream);
+
+/*
+ * svdq_group_norm -- channels-last group norm with an activation: the norm in
+ * front of the projections of a U-Net or an image decoder.  (The pages quantize
+ * such models and do not define their norms; the usual definition is taken.)
+ *   y = act((x - mean) / sqrt(var + eps) * gamma[c] + beta[c])
+ * with mean and (biased) variance over the S rows of a sample and the C / G
+ * channels of a group, in float32; rounded once to the type of X.
+ *   X     [in]  type, B samples of S rows of C channels, rows at pitch ldx
+ *               (sample b starts at row b S).
+ *   gamma, beta [in] float32, C, or NULL (1 and 0).
+ *   eps >= 0, act an svdq_act.
+ *   Y     [out] type, rows at pitch ldy (channels past C are not touched); Y may be X.
+ *   workspace [in/out] svdq_group_norm_workspace_bytes(B, S, C, G) bytes; zero it
+ *               once after allocating it (and again after a call that reported
+ *               SVDQ_ERR_TIMEOUT); calls that may overlap need their own.
+ * Shapes: C % G == 0, C <= 4096; any S and B (0 launches nothing), any pitch >= C.
+ * Values whose squared deviation leaves float32's range give a non-finite result.
+ */
+typedef enum {
+    SVDQ_ACT_NONE = 0,
+    SVDQ_ACT_SILU = 1,     /* y / (1 + exp(-y)) */
+    SVDQ_ACT_GELU = 2      /* the GELU of svdq_gelu_bf16, before its rounding */
+} svdq_act;
+SVDQ_API size_t svdq_group_norm_workspace_bytes(int64_t B, int64_t S, int64_t C, int64_t G);
+SVDQ_API svdq_status svdq_group_norm(const void* X, int type, int64_t ldx, int64_t B, int64_t S, int64_t C, int64_t G,
+                                     const float* gamma, const float* beta, float eps, int act, void* Y, int64_t ldy,
+                                     void* workspace, size_t workspace_bytes, svdq_stream_t stream);
+
+/*
+ * svdq_group_norm_quantize_i8 -- svdq_group_norm whose result, in float32 and not
+ * rounded to 16 bits, is quantized as svdq_quantize_act_i8 quantizes (smoothing
+ * inv_s, float32 of C, or NULL): Xq int8 (B S) x C and sx float32 (B S), the
+ * inputs of svdq_linear_i8 with M = B S and K = C.  Requires C % 16 == 0.
+ */
+SVDQ_API svdq_status svdq_group_norm_quantize_i8(const void* X, int type, int64_t ldx, int64_t B, int64_t S, int64_t C,
+                                                 int64_t G, const float* gamma, const float* beta, float eps, int act,
+                                                 const float* inv_s, int8_t* Xq, float* sx, void* workspace,
+                                                 size_t workspace_bytes, svdq_stream_t stream);
+
+/*
  * Calibration on the GPU ("From SmoothQuant to SVDQuant", quantization scheme:
  * the smoothing factors, the low-rank split and the activation global scale are
  * fixed offline from calibration data; section Smooth Quant (W8A8): the

@@ -1,0 +1,236 @@
+"""Channels-last group norm on the GPU, and its quantized form in front of the int8 layer, against float64."""
+import numpy as np
+import pytest
+import torch
+
+from helpers import require_gpu
+from oracle import int8 as O
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+
+
+def _lib():
+    from w4a4_rank_absorbed_b200 import svdq as C
+    return C
+
+
+def value_bound(x, G, gamma, beta, eps, act):
+    """(exact y, largest error of the float32 value), element by element.
+
+    Statistics: sums of deviations d from a pivot inside the channel's range D = max |x - mean| of the group, in
+    at most n = 4096 float32 steps one after another (a thread's run, then trees), each off by U of what it has
+    summed: mean off by em <= 2 n U D; the variance by 4 n U D^2 (worst case; a random walk gives sqrt(n)), so
+    1/sqrt by er = 2 n U D^2 / (var + eps) relative, plus 4 U for the root and the division.
+    Value: (x - mean) off by em + U |x - mean|, times rstd and gamma (3 U), plus beta (U of the result).
+    Activation: its slope is at most 1.13, and its own evaluation is off by 16 U (1 + |y|) at most."""
+    x = np.asarray(x, dtype=np.float64)
+    B, S, C = x.shape
+    g = x.reshape(B, S, G, C // G)
+    mean = g.mean(axis=(1, 3), keepdims=True)
+    var = ((g - mean) ** 2).mean(axis=(1, 3), keepdims=True)
+    D = np.abs(g - mean).max(axis=(1, 3), keepdims=True)
+    n = min(4096, 16 + S * (C // G))
+    rstd = 1.0 / np.sqrt(var + eps)
+    em = 2 * n * U * D + U * np.abs(mean)
+    er = 2 * n * U * D ** 2 / (var + eps) + 4 * U
+    z = np.abs(g - mean) * rstd
+    e = (em * rstd + z * (er + 4 * U)).reshape(B, S, C)
+    ga = np.ones(C) if gamma is None else np.abs(gamma.astype(np.float64))
+    y0 = O.group_norm(x, G, gamma, beta, eps, "none")
+    e = e * ga + 2 * U * (np.abs(y0) + (0 if beta is None else np.abs(beta)))
+    if act != "none":
+        e = 1.13 * e + 16 * U * (1 + np.abs(y0))
+    return O.group_norm(x, G, gamma, beta, eps, act), e
+
+
+def _case(B, S, C, kind, seed, offset=1.0):
+    r = np.random.default_rng(seed)
+    x = r.normal(size=(B, S, C)) * r.uniform(0.3, 2.0, C) + offset * r.uniform(-1, 1, C)
+    X = torch.from_numpy(x).to(TYPES[kind]).cuda()
+    gamma, beta = r.uniform(0.5, 1.5, C).astype(np.float32), r.normal(0, 0.3, C).astype(np.float32)
+    return X, gamma, beta
+
+
+def _run(X, B, S, C, G, gamma, beta, eps, act, Y=None):
+    L = _lib()
+    Y = torch.empty_like(X) if Y is None else Y
+    ws = L.new_group_norm_workspace(B, S, C, G)
+    a = {"none": L.SVDQ_ACT_NONE, "silu": L.SVDQ_ACT_SILU, "gelu": L.SVDQ_ACT_GELU}[act]
+    dev = lambda v: None if v is None else torch.from_numpy(v).cuda()  # noqa: E731
+    L.svdq_group_norm(X, B, S, C, G, dev(gamma), dev(beta), eps, a, Y, ws)
+    torch.cuda.synchronize()
+    assert L.svdq_get_device_error() == (0, 0)
+    return Y
+
+
+def _check(Y, X, G, gamma, beta, eps, act, kind):
+    y, e = value_bound(X.double().cpu().numpy(), G, gamma, beta, eps, act)
+    half = {"bf16": 2.0 ** -8, "fp16": 2.0 ** -11, "fp32": 0.0}[kind]
+    bound = e + half * (np.abs(y) + e) + (2.0 ** -25 if kind == "fp16" else 2.0 ** -149)
+    err = np.abs(Y.double().cpu().numpy() - y)
+    assert np.all(err <= bound), (float((err / bound).max()), np.unravel_index(int((err / bound).argmax()), err.shape))
+
+
+# one row and one channel a group up to several samples; channels that fill whole 16-byte vectors and not;
+# groups that straddle them (10 channels); rows that split over many blocks, and few
+SHAPES = [(1, 1, 8, 1), (1, 1, 1, 1), (2, 1, 64, 32), (1, 3, 30, 3), (1, 64, 320, 32), (2, 100, 33, 11), (3, 49, 320, 32),
+          (1, 1000, 128, 32), (2, 1024, 1280, 32), (1, 4099, 64, 4), (5, 77, 640, 32), (1, 500, 4096, 32), (1, 7, 4096, 1),
+          (2, 333, 2560, 32), (150, 5, 48, 6), (300, 2, 16, 16), (1, 40000, 8, 2), (4, 2048, 256, 8), (1, 257, 1001, 7)]
+
+
+@pytest.mark.parametrize("B,S,C,G", SHAPES)
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "fp32"])
+def test_group_norm(B, S, C, G, kind):
+    act = ["none", "silu", "gelu"][(B + S + C) % 3]
+    X, gamma, beta = _case(B, S, C, kind, S + C)
+    Y = _run(X, B, S, C, G, gamma, beta, 1e-5, act)
+    _check(Y, X, G, gamma, beta, 1e-5, act, kind)
+
+
+@pytest.mark.parametrize("act", ["none", "silu", "gelu"])
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "fp32"])
+def test_activations_without_affine(act, kind):
+    X, _, _ = _case(2, 300, 96, kind, 11)
+    _check(_run(X, 2, 300, 96, 12, None, None, 1e-6, act), X, 12, None, None, 1e-6, act, kind)
+
+
+@pytest.mark.parametrize("offset", [100.0, 3000.0])
+def test_means_far_from_zero(offset):
+    """The variance of values whose mean is many deviations away (no difference of large squares)."""
+    X, gamma, beta = _case(1, 2000, 64, "fp32", 12, offset)
+    X += offset
+    _check(_run(X, 1, 2000, 64, 8, gamma, beta, 1e-5, "none"), X, 8, gamma, beta, 1e-5, "none", "fp32")
+
+
+def test_constant_groups_and_zero_eps():
+    X = torch.full((1, 50, 32), 5.0, device="cuda")
+    beta = np.arange(32, dtype=np.float32)
+    Y = _run(X, 1, 50, 32, 4, None, beta, 1e-5, "none")
+    assert np.array_equal(Y.cpu().numpy()[0], np.broadcast_to(beta, (50, 32)))
+    X[:, :, 0] = 6.0
+    _check(_run(X, 1, 50, 32, 4, None, beta, 1e-5, "none"), X, 4, None, beta, 1e-5, "none", "fp32")
+    X2 = torch.randn(1, 50, 32, device="cuda")
+    _check(_run(X2, 1, 50, 32, 4, None, None, 0.0, "none"), X2, 4, None, None, 0.0, "none", "fp32")
+
+
+def test_non_finite_values_stay_in_their_group():
+    X = torch.randn(2, 200, 64, device="cuda")
+    clean = _run(X, 2, 200, 64, 8, None, None, 1e-5, "silu")
+    X[0, 17, 3] = float("nan")
+    X[1, 100, 63] = float("inf")
+    Y = _run(X, 2, 200, 64, 8, None, None, 1e-5, "silu")
+    assert bool(Y[0, :, :8].isnan().all()) and torch.equal(Y[0, :, 8:], clean[0, :, 8:])
+    assert not bool(Y[1, :, 56:].isfinite().any()) and torch.equal(Y[1, :, :56], clean[1, :, :56])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+@pytest.mark.parametrize("C,lead,pitch", [(64, 0, 96), (64, 8, 80), (33, 3, 41), (320, 16, 648)])
+def test_pitches_and_in_place(kind, C, lead, pitch):
+    """X a slice of a wider tensor (any pitch), Y another, and Y the same memory as X."""
+    if (lead * (2 if kind == "bf16" else 4)) % 16:
+        lead = 0
+    B, S, G = 2, 70, 1 if C == 33 else 4
+    X, gamma, beta = _case(B, S, C, kind, 13)
+    wide = torch.full((B, S, pitch), 9.0, dtype=TYPES[kind], device="cuda")
+    Xs = wide[:, :, lead:lead + C]
+    Xs.copy_(X)
+    out = torch.full((B, S, C + 5), 4.0, dtype=TYPES[kind], device="cuda")
+    Y = _run(Xs, B, S, C, G, gamma, beta, 1e-5, "silu", out[:, :, :C])
+    _check(Y, X, G, gamma, beta, 1e-5, "silu", kind)
+    assert bool((out[:, :, C:] == 4.0).all()) and torch.equal(Xs, X)
+    Y2 = _run(Xs, B, S, C, G, gamma, beta, 1e-5, "silu", Xs)
+    assert torch.equal(Y2, Y)
+    assert bool((wide[:, :, :lead] == 9.0).all()) and bool((wide[:, :, lead + C:] == 9.0).all())
+
+
+@pytest.mark.parametrize("B,S,C,G", [(1, 1, 16, 1), (1, 64, 320, 32), (2, 100, 48, 3), (3, 333, 640, 32), (1, 2000, 1280, 32),
+                                     (2, 17, 4096, 32), (160, 3, 64, 4), (1, 5000, 80, 10)])
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "fp32"])
+def test_quantized_norm(B, S, C, G, kind):
+    """Scales within the value's bound; each code within half a step and that bound of the exact value."""
+    L = _lib()
+    act = ["none", "silu", "gelu"][(B + S) % 3]
+    X, gamma, beta = _case(B, S, C, kind, 21)
+    inv_s = np.random.default_rng(5).uniform(0.3, 3.0, C).astype(np.float32)
+    Xq = torch.empty((B * S, C), dtype=torch.int8, device="cuda")
+    sx = torch.empty(B * S, dtype=torch.float32, device="cuda")
+    ws = L.new_group_norm_workspace(B, S, C, G)
+    L.svdq_group_norm_quantize_i8(X, B, S, C, G, torch.from_numpy(gamma).cuda(), torch.from_numpy(beta).cuda(), 1e-5,
+                                  {"none": 0, "silu": 1, "gelu": 2}[act], torch.from_numpy(inv_s).cuda(), Xq, sx, ws)
+    assert L.svdq_get_device_error() == (0, 0)
+    y, e = value_bound(X.double().cpu().numpy(), G, gamma, beta, 1e-5, act)
+    y, e = (v.reshape(B * S, C) * inv_s.astype(np.float64) for v in (y, e))
+    e = e + U * np.abs(y)
+    s = sx.double().cpu().numpy()
+    top, etop = np.abs(y).max(1), e.max(1)
+    assert np.all(np.abs(127 * s - top) <= etop + 2 * U * top)
+    q = Xq.double().cpu().numpy()
+    # |q s - y|: half a step, the value's error, and 127 s against the row's top (127 / a and its product: 3 U of |y|)
+    assert np.all(np.abs(q * s[:, None] - y) <= 0.5 * s[:, None] + e + 3 * U * np.abs(y) + 127 * U * s[:, None])
+
+
+def test_norm_into_the_layer():
+    """GroupNorm -> W8A8Linear as a model runs them: the fused input against the norm's float32 values quantized
+    by the layer.  The two sum in the same order, so the codes are the same; only the call differs."""
+    from w4a4_rank_absorbed_b200.calib import calibrate_w8a8
+    from w4a4_rank_absorbed_b200.layer import GroupNorm, W8A8Linear
+    r = np.random.default_rng(31)
+    B, H, Wd, C, N = 2, 13, 9, 320, 200
+    pic = torch.from_numpy(r.normal(size=(B, C, H, Wd))).float().cuda().to(memory_format=torch.channels_last)
+    X = pic.permute(0, 2, 3, 1)
+    norm = GroupNorm(32, C, torch.rand(C) + 0.5, torch.randn(C) * 0.1, act="silu")
+    Xn = norm(X)
+    L = W8A8Linear(calibrate_w8a8(Xn.reshape(-1, C).cpu(), r.normal(0, 0.05, (C, N)), bias=r.normal(size=N)))
+    Y = L.forward_norm(X, norm)
+    assert tuple(Y.shape) == (B, H, Wd, N)
+    assert torch.equal(Y, L(Xn))
+    ref = torch.nn.functional.silu(torch.nn.functional.group_norm(pic.double(), 32, norm.weight.double(),
+                                                                  norm.bias.double(), 1e-5)).permute(0, 2, 3, 1)
+    full = (ref * L.inv_s.double()).reshape(-1, C) @ (L.Wq.double() * L.sw.double()[:, None]).t() + L.bias.double()
+    # 8-bit activations: a code is off by half a step; over C of them the error of a row is about
+    # 0.29 step sqrt(C) |w|_rms, held here to the certain bound 0.51 step sum |w|
+    step = (ref * L.inv_s.double()).reshape(-1, C).abs().amax(1) / 127
+    bound = 0.51 * step[:, None] * (L.Wq.double() * L.sw.double()[:, None]).abs().sum(1)[None, :]
+    assert bool(((Y.reshape(-1, N).double() - full).abs() <= bound).all())
+    assert tuple(L.forward_norm(X[:0], norm).shape) == (0, H, Wd, N)
+
+
+def test_norm_on_streams_and_in_graphs():
+    from w4a4_rank_absorbed_b200.layer import GroupNorm
+    norm = GroupNorm(32, 640, act="silu")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    Xs = [torch.randn(2, 1024, 640, device="cuda", generator=g).to(torch.bfloat16) for _ in range(3)]
+    want = [norm(X) for X in Xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in Xs]
+    for _ in range(20):
+        got = [norm.forward(X, stream=s) for X, s in zip(Xs, streams)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graphs, outs = [], []
+    for X in Xs:
+        G = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(G):
+            outs.append(norm(X))
+        graphs.append(G)
+    for _ in range(20):
+        for G, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                G.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    assert _lib().svdq_get_device_error() == (0, 0)
+
+
+def test_the_same_call_gives_the_same_bits():
+    X, gamma, beta = _case(2, 3000, 320, "fp32", 41)
+    Y = _run(X, 2, 3000, 320, 32, gamma, beta, 1e-5, "silu")
+    assert all(torch.equal(Y, _run(X, 2, 3000, 320, 32, gamma, beta, 1e-5, "silu")) for _ in range(10))

@@ -127,6 +127,31 @@ def calibrate(X, W, r: int, alpha: float = 0.5, bias=None, lora_A=None, lora_B=N
                      bias=None if bias is None else _as64(bias).to(torch.bfloat16), s=s)
 
 
+@dataclass
+class W8A8Data:
+    """Constants of an 8-bit integer layer (layer.W8A8Linear): the smoothed weight, not yet packed."""
+    K: int
+    N: int
+    inv_s: Optional[torch.Tensor]   # float32 [K], or None (no smoothing)
+    W_hat: torch.Tensor             # float32 [K, N]: diag(s) W
+    bias: Optional[torch.Tensor]    # float32 [N]
+    s: torch.Tensor                 # float64 [K]
+
+
+def calibrate_w8a8(X, W, alpha: float = 0.5, bias=None, X_cal=None) -> W8A8Data:
+    """Smoothing of W (K x N) for activations X (M x K) as in calibrate ("From SmoothQuant to SVDQuant",
+    section Smooth Quant (W8A8)), without the low-rank split: both operands then go to 8 bits, with scales
+    that the packing and each forward pass find themselves, so nothing else needs calibrating."""
+    Wd = _as64(W)
+    Xc = _as64(X if X_cal is None else X_cal)
+    K, N = Wd.shape
+    ax, aw = Xc.abs().amax(dim=0), Wd.abs().amax(dim=1)
+    s = ax.pow(alpha) / aw.pow(1.0 - alpha)
+    s = torch.where((ax == 0) | (aw == 0), torch.ones_like(s), s)
+    return W8A8Data(K=K, N=N, inv_s=(1.0 / s).to(torch.float32), W_hat=(s[:, None] * Wd).to(torch.float32).contiguous(),
+                    bias=None if bias is None else _as64(bias).to(torch.float32), s=s)
+
+
 # ------------------------------------------------------------------ on the GPU --
 def randomized_rank_r(W_hat: torch.Tensor, r: int, oversample: int = 32, power_iters: int = 6,
                       seed: int = 0):

@@ -15,7 +15,9 @@
 #include "../../include/svdq.h"
 #include "common.cuh"
 #include "calib.cuh"
+#include "group_norm.cuh"
 #include "linear.cuh"
+#include "linear_i8.cuh"
 #include "pack_weight.cuh"
 #include "quantize_act.cuh"
 
@@ -443,6 +445,121 @@ svdq_status linear_impl(const uint8_t* Xq, const uint8_t* SFx, float gs_x, const
   return launch_status();
 }
 
+// ------------------------------------------------------------- int8 layer ---
+constexpr int64_t kMaxK8 = int64_t(1) << 17;      // 128 * 128 * K stays inside the 32-bit sum below this
+
+size_t dtype_size(int type) { return type == SVDQ_FP32 ? 4 : 2; }
+bool dtype_ok(int type) { return type == SVDQ_BF16 || type == SVDQ_FP32 || type == SVDQ_FP16; }
+
+svdq_status check_shape_i8(int64_t M, int64_t N, int64_t K) {
+  if (M < 0 || N < 1 || K < 1) return SVDQ_ERR_INVALID_ARG;
+  if (M > kMaxDim || N > kMaxDim || K >= kMaxK8 || K % 16 != 0) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+  return SVDQ_OK;
+}
+
+// Rows of `width` elements at pitch ld, at `p`: NULL, pitch and alignment (row_align: every row on 16 bytes).
+svdq_status check_rows(const void* p, int type, int64_t width, int64_t ld, bool row_align) {
+  if (!p || ld < width) return SVDQ_ERR_INVALID_ARG;
+  if (ld > (int64_t(1) << 40)) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(p) || (row_align && ((uint64_t)ld * dtype_size(type)) % 16 != 0)) return SVDQ_ERR_MISALIGNED;
+  return SVDQ_OK;
+}
+
+svdq_status launch_quantize_i8(const void* X, int x_type, int64_t ldx, int64_t M, int64_t K, const float* inv_s,
+                               int8_t* Xq, float* sx, cudaStream_t s) {
+  cudaError_t e;
+  if (x_type == SVDQ_BF16)
+    e = launch_pdl(k_quantize_act_i8<__nv_bfloat16>, dim3((unsigned)M), dim3(256), 0, s, 1,
+                   static_cast<const __nv_bfloat16*>(X), (int)K, ldx, inv_s, Xq, sx);
+  else if (x_type == SVDQ_FP16)
+    e = launch_pdl(k_quantize_act_i8<__half>, dim3((unsigned)M), dim3(256), 0, s, 1, static_cast<const __half*>(X),
+                   (int)K, ldx, inv_s, Xq, sx);
+  else
+    e = launch_pdl(k_quantize_act_i8<float>, dim3((unsigned)M), dim3(256), 0, s, 1, static_cast<const float*>(X),
+                   (int)K, ldx, inv_s, Xq, sx);
+  return e == cudaSuccess ? launch_status() : SVDQ_ERR_CUDA;
+}
+
+svdq_status launch_linear_i8(DevInfo* d, const int8_t* Xq, const float* sx, const int8_t* Wq, const float* sw,
+                             const float* bias, void* Y, int y_type, int64_t ldy, int64_t M, int64_t N, int64_t K,
+                             cudaStream_t s) {
+  (void)d;
+  LinearI8Args a;
+  a.sx = sx;
+  a.sw = sw;
+  a.bias = bias;
+  a.Y = Y;
+  a.y_type = y_type;
+  a.ldy = ldy;
+  a.M = (int)M;
+  a.N = (int)N;
+  a.K = (int)K;
+  const dim3 grid((unsigned)((M + 63) / 64), (unsigned)((N + 63) / 64));
+  if (launch_pdl(k_linear_i8, grid, dim3(256), 0, s, 1, Xq, Wq, a) != cudaSuccess) return SVDQ_ERR_CUDA;
+  return launch_status();
+}
+
+// ------------------------------------------------------------- group norm ---
+constexpr int64_t kMaxNormC = 4096;
+
+size_t group_norm_workspace(int64_t B, int64_t G) { return (size_t)B * (size_t)G * sizeof(float2); }
+
+struct NormArgs {
+  const void* X;
+  int type;
+  int64_t ldx, B, S, C, G;
+  const float *gamma, *beta;
+  float eps;
+  int act;
+  void* Y;
+  int64_t ldy;
+  const float* inv_s;
+  int8_t* Xq;
+  float* sx;
+  void* ws;
+  size_t ws_bytes;
+};
+
+template <typename T, bool QUANT>
+svdq_status launch_norm(const NormArgs& n, cudaStream_t s) {
+  const T* X = static_cast<const T*>(n.X);
+  float2* stats = static_cast<float2*>(n.ws);
+  if (launch_pdl(k_group_stats<T>, dim3((unsigned)(n.B * n.G)), dim3(256), 0, s, 1, X, n.S, (int)n.C, n.ldx, (int)n.G,
+                 n.eps, stats) != cudaSuccess ||
+      launch_pdl(k_group_apply<T, QUANT>, dim3((unsigned)(n.B * n.S)), dim3(256), 0, s, 1, X, n.S, (int)n.C, n.ldx,
+                 (int)n.G, (const float2*)stats, n.gamma, n.beta, n.act, static_cast<T*>(n.Y), n.ldy, n.inv_s, n.Xq,
+                 n.sx) != cudaSuccess)
+    return SVDQ_ERR_CUDA;
+  return launch_status();
+}
+
+template <bool QUANT>
+svdq_status norm_impl(const NormArgs& n, cudaStream_t s) {
+  if (n.B < 0 || n.S < 0 || n.C < 1 || n.G < 1 || !dtype_ok(n.type) || n.act < SVDQ_ACT_NONE ||
+      n.act > SVDQ_ACT_GELU || !(n.eps >= 0.0f) || !std::isfinite(n.eps))
+    return SVDQ_ERR_INVALID_ARG;
+  if (n.C % n.G != 0 || n.C > kMaxNormC || (QUANT && n.C % 16 != 0) || n.B > kMaxDim || n.S > kMaxDim ||
+      (n.B > 0 && n.S > kMaxDim / n.B))
+    return SVDQ_ERR_UNSUPPORTED_SHAPE;
+  if (n.B == 0 || n.S == 0) return SVDQ_OK;        // an empty batch: nothing to launch
+  svdq_status st = check_rows(n.X, n.type, n.C, n.ldx, false);
+  if (st != SVDQ_OK) return st;
+  if (QUANT) {
+    if (!n.Xq || !n.sx) return SVDQ_ERR_INVALID_ARG;
+    if (!aligned16(n.Xq) || !aligned16(n.sx) || (n.inv_s && !aligned16(n.inv_s))) return SVDQ_ERR_MISALIGNED;
+  } else if ((st = check_rows(n.Y, n.type, n.C, n.ldy, false)) != SVDQ_OK) {
+    return st;
+  }
+  if (!n.ws || n.ws_bytes < group_norm_workspace(n.B, n.G)) return SVDQ_ERR_INVALID_ARG;
+  if (!aligned16(n.ws) || (n.gamma && !aligned16(n.gamma)) || (n.beta && !aligned16(n.beta))) return SVDQ_ERR_MISALIGNED;
+  int dev;
+  DevInfo* d;
+  if ((st = current_device(&dev, &d)) != SVDQ_OK) return st;
+  if (n.type == SVDQ_BF16) return launch_norm<__nv_bfloat16, QUANT>(n, s);
+  if (n.type == SVDQ_FP16) return launch_norm<__half, QUANT>(n, s);
+  return launch_norm<float, QUANT>(n, s);
+}
+
 }  // namespace
 
 extern "C" {
@@ -596,6 +713,100 @@ svdq_status svdq_gelu_bf16(const uint16_t* X, int64_t n, uint16_t* Y, svdq_strea
       cudaSuccess)
     return SVDQ_ERR_CUDA;
   return launch_status();
+}
+
+svdq_status svdq_pack_weight_i8(const float* W_hat, int64_t K, int64_t N, int8_t* Wq, float* sw, svdq_stream_t stream) {
+  svdq_status st = check_shape_i8(1, N, K);
+  if (st != SVDQ_OK) return st;
+  if (!W_hat || !Wq || !sw) return SVDQ_ERR_INVALID_ARG;
+  if (!aligned16(W_hat) || !aligned16(Wq) || !aligned16(sw)) return SVDQ_ERR_MISALIGNED;
+  int dev;
+  DevInfo* d;
+  if ((st = current_device(&dev, &d)) != SVDQ_OK) return st;
+  k_pack_weight_i8<<<(unsigned)((N + 31) / 32), PW8_THREADS, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+      W_hat, (int)K, (int)N, Wq, sw);
+  return launch_status();
+}
+
+svdq_status svdq_quantize_act_i8(const void* X, int x_type, int64_t ldx, int64_t M, int64_t K, const float* inv_s,
+                                 int8_t* Xq, float* sx, svdq_stream_t stream) {
+  svdq_status st = check_shape_i8(M, 1, K);
+  if (st != SVDQ_OK) return st;
+  if (!dtype_ok(x_type)) return SVDQ_ERR_INVALID_ARG;
+  if (M == 0) return SVDQ_OK;                 // an empty batch: nothing to launch
+  if ((st = check_rows(X, x_type, K, ldx, true)) != SVDQ_OK) return st;
+  if (!Xq || !sx) return SVDQ_ERR_INVALID_ARG;
+  if (!aligned16(Xq) || !aligned16(sx) || (inv_s && !aligned16(inv_s))) return SVDQ_ERR_MISALIGNED;
+  int dev;
+  DevInfo* d;
+  if ((st = current_device(&dev, &d)) != SVDQ_OK) return st;
+  return launch_quantize_i8(X, x_type, ldx, M, K, inv_s, Xq, sx, reinterpret_cast<cudaStream_t>(stream));
+}
+
+svdq_status svdq_linear_i8(const int8_t* Xq, const float* sx, const int8_t* Wq, const float* sw, const float* bias,
+                           void* Y, int y_type, int64_t ldy, int64_t M, int64_t N, int64_t K, svdq_stream_t stream) {
+  svdq_status st = check_shape_i8(M, N, K);
+  if (st != SVDQ_OK) return st;
+  if (!dtype_ok(y_type)) return SVDQ_ERR_INVALID_ARG;
+  if (M == 0) return SVDQ_OK;                 // an empty batch: nothing to launch
+  if (!Xq || !sx || !Wq || !sw) return SVDQ_ERR_INVALID_ARG;
+  if (!aligned16(Xq) || !aligned16(sx) || !aligned16(Wq) || !aligned16(sw) || (bias && !aligned16(bias)))
+    return SVDQ_ERR_MISALIGNED;
+  if ((st = check_rows(Y, y_type, N, ldy, false)) != SVDQ_OK) return st;
+  int dev;
+  DevInfo* d;
+  if ((st = current_device(&dev, &d)) != SVDQ_OK) return st;
+  return launch_linear_i8(d, Xq, sx, Wq, sw, bias, Y, y_type, ldy, M, N, K, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t svdq_forward_i8_workspace_bytes(int64_t M, int64_t K) {
+  if (M < 1 || check_shape_i8(M, 1, K) != SVDQ_OK) return 0;
+  return (size_t)M * (size_t)K + (size_t)M * sizeof(float);
+}
+
+svdq_status svdq_forward_i8(const void* X, int x_type, int64_t ldx, const float* inv_s, const int8_t* Wq,
+                            const float* sw, const float* bias, void* Y, int y_type, int64_t ldy, int64_t M, int64_t N,
+                            int64_t K, void* workspace, size_t workspace_bytes, svdq_stream_t stream) {
+  svdq_status st = check_shape_i8(M, N, K);
+  if (st != SVDQ_OK) return st;
+  if (!dtype_ok(x_type) || !dtype_ok(y_type)) return SVDQ_ERR_INVALID_ARG;
+  if (M == 0) return SVDQ_OK;                 // an empty batch: nothing to launch
+  if ((st = check_rows(X, x_type, K, ldx, true)) != SVDQ_OK || (st = check_rows(Y, y_type, N, ldy, false)) != SVDQ_OK)
+    return st;
+  if (!Wq || !sw || !workspace || workspace_bytes < svdq_forward_i8_workspace_bytes(M, K)) return SVDQ_ERR_INVALID_ARG;
+  if (!aligned16(Wq) || !aligned16(sw) || (bias && !aligned16(bias)) || (inv_s && !aligned16(inv_s)) ||
+      !aligned16(workspace))
+    return SVDQ_ERR_MISALIGNED;
+  int dev;
+  DevInfo* d;
+  if ((st = current_device(&dev, &d)) != SVDQ_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int8_t* Xq = static_cast<int8_t*>(workspace);           // M x K codes (K % 16 == 0), then the M scales
+  float* sx = reinterpret_cast<float*>(Xq + (size_t)M * (size_t)K);
+  if ((st = launch_quantize_i8(X, x_type, ldx, M, K, inv_s, Xq, sx, s)) != SVDQ_OK) return st;
+  return launch_linear_i8(d, Xq, sx, Wq, sw, bias, Y, y_type, ldy, M, N, K, s);
+}
+
+size_t svdq_group_norm_workspace_bytes(int64_t B, int64_t S, int64_t C, int64_t G) {
+  if (B < 1 || S < 1 || C < 1 || G < 1 || C % G != 0 || C > kMaxNormC || B > kMaxDim) return 0;
+  return group_norm_workspace(B, G);
+}
+
+svdq_status svdq_group_norm(const void* X, int type, int64_t ldx, int64_t B, int64_t S, int64_t C, int64_t G,
+                            const float* gamma, const float* beta, float eps, int act, void* Y, int64_t ldy,
+                            void* workspace, size_t workspace_bytes, svdq_stream_t stream) {
+  const NormArgs n = {X, type, ldx, B, S, C, G, gamma, beta, eps, act, Y, ldy, nullptr, nullptr, nullptr, workspace,
+                      workspace_bytes};
+  return norm_impl<false>(n, reinterpret_cast<cudaStream_t>(stream));
+}
+
+svdq_status svdq_group_norm_quantize_i8(const void* X, int type, int64_t ldx, int64_t B, int64_t S, int64_t C,
+                                        int64_t G, const float* gamma, const float* beta, float eps, int act,
+                                        const float* inv_s, int8_t* Xq, float* sx, void* workspace,
+                                        size_t workspace_bytes, svdq_stream_t stream) {
+  const NormArgs n = {X, type, ldx, B, S, C, G, gamma, beta, eps, act, nullptr, 0, inv_s, Xq, sx, workspace,
+                      workspace_bytes};
+  return norm_impl<true>(n, reinterpret_cast<cudaStream_t>(stream));
 }
 
 svdq_status svdq_calib_absmax_cols(const uint16_t* X, int64_t M, int64_t K, float* amax_x, int accumulate,

@@ -1,4 +1,5 @@
-"""SVDQLinear: a packed SVDQuant W4A4 linear layer on one B200.
+"""SVDQLinear: a packed SVDQuant W4A4 linear layer on one B200; W8A8Linear, its 8-bit integer
+counterpart (SmoothQuant W8A8); GroupNorm, the channels-last norm in front of either.
 
 Holds the packed residual weight and the low-rank factors in device memory
 and runs the forward pass as two launches of the CUDA library
@@ -12,13 +13,14 @@ torch is used for device memory and streams only.
 """
 from __future__ import annotations
 
+import contextlib
 from typing import Dict, Optional
 
 import numpy as np
 import torch
 
 from . import svdq as _C
-from .calib import LayerData
+from .calib import LayerData, W8A8Data
 
 
 def _f32(x) -> float:
@@ -250,3 +252,219 @@ class SVDQMLP:
         return fc2.forward(X2, out=out, stream=stream)
 
     __call__ = forward
+
+
+# ------------------------------------------------------------------ int8 layer and group norm --
+def _on_stream(stream, device: torch.device):
+    """Context that makes `stream` (a torch stream, a raw handle or None) torch's current one, so that what
+    is allocated inside belongs to it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
+def _used_here(*tensors) -> None:
+    """Tell torch's allocator that the current stream uses these tensors (their memory is not handed out
+    again before the work queued so far on it is done, whatever stream they were allocated on)."""
+    for t in tensors:
+        if t is not None:
+            t.record_stream(torch.cuda.current_stream(t.device))
+
+
+class GroupNorm:
+    """Channels-last group norm with an activation ("none", "silu" or "gelu"): X [B, ..., C] of bf16, fp16
+    or fp32 -> the same shape and type.  weight and bias are float32 [C] (None: 1 and 0).  A picture held
+    as [B, C, H, W] in torch's channels_last format is X = picture.permute(0, 2, 3, 1)."""
+
+    _ACTS = {"none": _C.SVDQ_ACT_NONE, "silu": _C.SVDQ_ACT_SILU, "gelu": _C.SVDQ_ACT_GELU}
+
+    def __init__(self, num_groups: int, num_channels: int, weight: Optional[torch.Tensor] = None,
+                 bias: Optional[torch.Tensor] = None, eps: float = 1e-5, act: str = "none",
+                 device: Optional[torch.device] = None):
+        if num_groups < 1 or num_channels < 1 or num_channels % num_groups:
+            raise ValueError(f"{num_channels} channels do not divide into {num_groups} groups")
+        if act not in self._ACTS:
+            raise ValueError(f"act must be one of {sorted(self._ACTS)}, got {act!r}")
+        for t, name in ((weight, "weight"), (bias, "bias")):
+            if t is not None and tuple(t.shape) != (num_channels,):
+                raise ValueError(f"{name} must have {num_channels} elements")
+        dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        if dev.type == "cuda" and dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        self.device, self.G, self.C, self.eps, self.act = dev, num_groups, num_channels, float(eps), self._ACTS[act]
+        self.weight = None if weight is None else weight.to(dev, torch.float32).contiguous()
+        self.bias = None if bias is None else bias.to(dev, torch.float32).contiguous()
+        self._ws: Dict[tuple, torch.Tensor] = {}
+
+    def _rows(self, X: torch.Tensor):
+        if X.dim() < 2 or X.shape[-1] != self.C:
+            raise ValueError(f"X must be [B, ..., {self.C}], got {tuple(X.shape)}")
+        check_device(X, self.device, "X")
+        B = X.shape[0]
+        S = 1
+        for n in X.shape[1:-1]:
+            S *= n
+        return B, S
+
+    def _workspace(self, B: int, S: int):
+        """One workspace per stream and shape.  A call that is being captured gets one of its own, zeroed
+        inside the graph: graphs replayed at the same time share none."""
+        if B == 0 or S == 0:
+            return None
+        if torch.cuda.is_current_stream_capturing():
+            return _C.new_group_norm_workspace(B, S, self.C, self.G, self.device)
+        key = (torch.cuda.current_stream(self.device).cuda_stream, B, S)
+        ws = self._ws.get(key)
+        if ws is None:
+            ws = self._ws[key] = _C.new_group_norm_workspace(B, S, self.C, self.G, self.device)
+        return ws
+
+    def forward(self, X: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        B, S = self._rows(X)
+        with torch.cuda.device(self.device), _on_stream(stream, self.device):
+            if out is None:
+                out = torch.empty(X.shape, dtype=X.dtype, device=self.device)
+            elif out.shape != X.shape:
+                raise ValueError(f"out has shape {tuple(out.shape)}, X {tuple(X.shape)}")
+            _C.svdq_group_norm(X, B, S, self.C, self.G, self.weight, self.bias, self.eps, self.act, out,
+                               self._workspace(B, S))
+            if stream is not None:
+                _used_here(X, out)
+        return out
+
+    __call__ = forward
+
+    def quantize(self, X: torch.Tensor, inv_s: Optional[torch.Tensor] = None, stream=None):
+        """The norm's result in 8 bits: codes int8 [rows, C] and scales float32 [rows], for W8A8Linear.gemm
+        (inv_s: that layer's smoothing factors)."""
+        B, S = self._rows(X)
+        with torch.cuda.device(self.device), _on_stream(stream, self.device):
+            Xq = torch.empty((B * S, self.C), dtype=torch.int8, device=self.device)
+            sx = torch.empty(B * S, dtype=torch.float32, device=self.device)
+            _C.svdq_group_norm_quantize_i8(X, B, S, self.C, self.G, self.weight, self.bias, self.eps, self.act, inv_s,
+                                           Xq, sx, self._workspace(B, S))
+            if stream is not None:
+                _used_here(X, inv_s)
+        return Xq, sx
+
+
+class W8A8Linear:
+    """The 8-bit integer layer (SmoothQuant W8A8) on one B200, for the layers that four bits harm:
+
+        svdq_quantize_act_i8   X (bf16, fp16 or fp32)  ->  Xq int8, sx per token
+        svdq_linear_i8         Xq, sx, Wq int8, sw per channel, bias  ->  Y (bf16, fp16 or fp32)
+
+    forward runs both in one call of the library (svdq_forward_i8); forward_norm takes its 8-bit input
+    straight from a GroupNorm.  Work buffers come from torch's allocator on the stream of the call, so calls
+    on several streams and captured graphs share none."""
+
+    _PACKED = ("Wq", "sw", "inv_s", "bias")
+
+    def __init__(self, data: W8A8Data, device: Optional[torch.device] = None, stream=None):
+        dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        if dev.type == "cuda" and dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        self.device, self.K, self.N = dev, data.K, data.N
+        with torch.cuda.device(dev):
+            s = None if stream is None else stream if isinstance(stream, torch.cuda.Stream) else \
+                torch.cuda.ExternalStream(_C.stream_handle(stream), device=dev)
+            if s is not None:
+                s.wait_stream(torch.cuda.current_stream(dev))
+            with _on_stream(s, dev):
+                W = data.W_hat.to(dev, torch.float32).contiguous()
+                self.Wq = torch.empty((self.N, self.K), dtype=torch.int8, device=dev)
+                self.sw = torch.empty(self.N, dtype=torch.float32, device=dev)
+                _C.svdq_pack_weight_i8(W, self.K, self.N, self.Wq, self.sw)
+                self.inv_s = None if data.inv_s is None else data.inv_s.to(dev, torch.float32).contiguous()
+                self.bias = None if data.bias is None else data.bias.to(dev, torch.float32).contiguous()
+            if s is not None:
+                torch.cuda.current_stream(dev).wait_stream(s)
+
+    def state_dict(self) -> Dict[str, object]:
+        """The packed layer as host tensors and sizes (W8A8Linear.from_state_dict rebuilds it)."""
+        out: Dict[str, object] = {"K": self.K, "N": self.N}
+        for k in self._PACKED:
+            t = getattr(self, k)
+            out[k] = None if t is None else t.detach().cpu()
+        return out
+
+    @classmethod
+    def from_state_dict(cls, state: Dict[str, object], device: Optional[torch.device] = None) -> "W8A8Linear":
+        self = cls.__new__(cls)
+        dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        if dev.type == "cuda" and dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        self.device, self.K, self.N = dev, int(state["K"]), int(state["N"])
+        expect = {"Wq": ((self.N, self.K), torch.int8), "sw": ((self.N,), torch.float32),
+                  "inv_s": ((self.K,), torch.float32), "bias": ((self.N,), torch.float32)}
+        for k, (shape, dtype) in expect.items():
+            t = state[k]
+            if t is None and k in ("Wq", "sw") or t is not None and (tuple(t.shape) != shape or t.dtype != dtype):
+                raise ValueError(f"state entry {k} must be {dtype} {shape}")
+            setattr(self, k, None if t is None else t.to(dev).contiguous())
+        return self
+
+    def _check(self, X: torch.Tensor) -> int:
+        if X.dim() < 1 or X.shape[-1] != self.K:
+            raise ValueError(f"X must be [..., {self.K}], got {tuple(X.shape)}")
+        check_device(X, self.device, "X")
+        return X.numel() // self.K
+
+    def _out(self, lead, out, dtype):
+        if out is None:
+            return torch.empty((*lead, self.N), dtype=dtype, device=self.device)
+        check_device(out, self.device, "out")
+        if tuple(out.shape) != (*lead, self.N):
+            raise ValueError(f"out must be {(*lead, self.N)}, got {tuple(out.shape)}")
+        return out
+
+    def quantize(self, X: torch.Tensor, stream=None):
+        """Codes int8 [rows, K] and scales float32 [rows] of X [..., K]."""
+        M = self._check(X)
+        with torch.cuda.device(self.device), _on_stream(stream, self.device):
+            Xq = torch.empty((M, self.K), dtype=torch.int8, device=self.device)
+            sx = torch.empty(M, dtype=torch.float32, device=self.device)
+            _C.svdq_quantize_act_i8(X, M, self.K, self.inv_s, Xq, sx)
+            if stream is not None:
+                _used_here(X)
+        return Xq, sx
+
+    def gemm(self, Xq: torch.Tensor, sx: torch.Tensor, Y: torch.Tensor, stream=None) -> torch.Tensor:
+        for t, name in ((Xq, "Xq"), (sx, "sx"), (Y, "Y")):
+            check_device(t, self.device, name)
+        with torch.cuda.device(self.device), _on_stream(stream, self.device):
+            _C.svdq_linear_i8(Xq, sx, self.Wq, self.sw, self.bias, Y, Xq.shape[0], self.N, self.K)
+            if stream is not None:
+                _used_here(Xq, sx, Y)
+        return Y
+
+    def forward(self, X: torch.Tensor, out: Optional[torch.Tensor] = None, dtype: Optional[torch.dtype] = None,
+                stream=None) -> torch.Tensor:
+        """Y = layer(X); X [..., K] on the device; returns [..., N] of `dtype` (default: the type of X)."""
+        M = self._check(X)
+        with torch.cuda.device(self.device), _on_stream(stream, self.device):
+            Y = self._out(X.shape[:-1], out, dtype or X.dtype)
+            ws = torch.empty(max(1, _C.svdq_forward_i8_workspace_bytes(M, self.K)), dtype=torch.uint8,
+                             device=self.device)
+            _C.svdq_forward_i8(X, M, self.K, self.inv_s, self.Wq, self.sw, self.bias, Y, self.N, ws)
+            if stream is not None:
+                _used_here(X, Y)
+        return Y
+
+    __call__ = forward
+
+    def forward_norm(self, X: torch.Tensor, norm: GroupNorm, out: Optional[torch.Tensor] = None,
+                     dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
+        """layer(norm(X)) with the norm's result quantized where it is computed; X [B, ..., K] channels last."""
+        self._check(X)
+        if norm.device != self.device:
+            raise ValueError(f"the norm is on {norm.device}, the layer on {self.device}")
+        with torch.cuda.device(self.device), _on_stream(stream, self.device):
+            Y = self._out(X.shape[:-1], out, dtype or X.dtype)
+            Xq, sx = norm.quantize(X, self.inv_s)
+            _C.svdq_linear_i8(Xq, sx, self.Wq, self.sw, self.bias, Y, Xq.shape[0], self.N, self.K)
+            if stream is not None:
+                _used_here(X, Y)
+        return Y

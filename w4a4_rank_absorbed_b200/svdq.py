@@ -43,7 +43,13 @@ EXPORTED = ("svdq_status_string", "svdq_version", "svdq_sf_bytes", "svdq_pack_we
             "svdq_mx_sf_bytes", "svdq_pack_weight_mx", "svdq_quantize_act_mx", "svdq_linear_mx",
             "svdq_linear_gelu_quantize", "svdq_linear_gelu_quantize_workspace_bytes", "svdq_gelu_bf16",
             "svdq_calib_absmax_cols", "svdq_calib_absmax_rows", "svdq_calib_smooth", "svdq_calib_scale_rows",
-            "svdq_calib_act_amax", "svdq_map_cache_stats", "svdq_build_flags")
+            "svdq_calib_act_amax", "svdq_map_cache_stats", "svdq_build_flags", "svdq_pack_weight_i8",
+            "svdq_quantize_act_i8", "svdq_linear_i8", "svdq_forward_i8", "svdq_forward_i8_workspace_bytes",
+            "svdq_group_norm", "svdq_group_norm_workspace_bytes", "svdq_group_norm_quantize_i8")
+
+SVDQ_BF16, SVDQ_FP32, SVDQ_FP16 = 0, 1, 2
+_DTYPES = {torch.bfloat16: SVDQ_BF16, torch.float32: SVDQ_FP32, torch.float16: SVDQ_FP16}
+SVDQ_ACT_NONE, SVDQ_ACT_SILU, SVDQ_ACT_GELU = 0, 1, 2
 
 
 class SVDQError(RuntimeError):
@@ -117,6 +123,20 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
                        ("svdq_calib_act_amax", [_P, _I64, _I64, _P, _P, _I, _P])):
         getattr(lib, name).restype = _I
         getattr(lib, name).argtypes = args
+    _Z = ctypes.c_size_t
+    for name, args in (("svdq_pack_weight_i8", [_P, _I64, _I64, _P, _P, _P]),
+                       ("svdq_quantize_act_i8", [_P, _I, _I64, _I64, _I64, _P, _P, _P, _P]),
+                       ("svdq_linear_i8", [_P, _P, _P, _P, _P, _P, _I, _I64, _I64, _I64, _I64, _P]),
+                       ("svdq_forward_i8", [_P, _I, _I64, _P, _P, _P, _P, _P, _I, _I64, _I64, _I64, _I64, _P, _Z, _P]),
+                       ("svdq_group_norm", [_P, _I, _I64, _I64, _I64, _I64, _I64, _P, _P, _F, _I, _P, _I64, _P, _Z, _P]),
+                       ("svdq_group_norm_quantize_i8", [_P, _I, _I64, _I64, _I64, _I64, _I64, _P, _P, _F, _I, _P, _P, _P,
+                                                        _P, _Z, _P])):
+        getattr(lib, name).restype = _I
+        getattr(lib, name).argtypes = args
+    lib.svdq_forward_i8_workspace_bytes.restype = _Z
+    lib.svdq_forward_i8_workspace_bytes.argtypes = [_I64, _I64]
+    lib.svdq_group_norm_workspace_bytes.restype = _Z
+    lib.svdq_group_norm_workspace_bytes.argtypes = [_I64, _I64, _I64, _I64]
     lib.svdq_build_flags.restype = _I
     lib.svdq_build_flags.argtypes = []
     lib.svdq_map_cache_stats.restype = None
@@ -375,3 +395,140 @@ def svdq_get_device_error(stream=None):
     site = _I(0)
     st = lib.svdq_get_device_error(_stream(stream), ctypes.byref(site))
     return int(st), int(site.value)
+
+
+# ------------------------------------------------- int8 layer and group norm --
+# These calls launch on the device of their first tensor, on `stream` or torch's current stream of
+# that device; tensors on another device, too small or of another type are refused here, since the
+# library sees raw pointers only.
+def _vec(t, dtype, n: int, dev: int, name: str) -> Optional[int]:
+    """Pointer of a contiguous tensor of at least n elements (None passes: an argument left out)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected dtype {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    if t.numel() < n:
+        raise ValueError(f"{name}: expected {n} elements, got {t.numel()}")
+    return t.data_ptr()
+
+
+def _rows(t, rows: int, width: int, dev: int, name: str):
+    """(pointer, element type, row pitch) of a tensor whose last axis is `width` contiguous elements and
+    whose leading axes are `rows` rows at one pitch."""
+    ty = _DTYPES.get(t.dtype)
+    if ty is None:
+        raise TypeError(f"{name}: expected bfloat16, float16 or float32, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    shape = t.shape
+    if t.numel() != rows * width or not shape or shape[-1] != width:
+        raise ValueError(f"{name}: expected {rows} rows of {width}, got {tuple(shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), ty, width
+    st = t.stride()
+    ld = 0                                         # the pitch: the innermost leading axis longer than 1 gives it
+    expect = 0
+    for i in range(len(shape) - 2, -1, -1):
+        if shape[i] != 1:
+            if ld == 0:
+                ld = expect = st[i]
+            if st[i] != expect:
+                raise ValueError(f"{name}: its rows are not at one pitch (strides {st})")
+        expect *= shape[i]
+    if (width > 1 and st[-1] != 1) or (rows > 1 and ld < width):
+        raise ValueError(f"{name}: expected rows of contiguous elements (strides {st})")
+    return t.data_ptr(), ty, max(ld, width)
+
+
+def _cuda_index(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    return t.get_device()
+
+
+def _call(name: str, dev: int, stream, *args) -> None:
+    fn = getattr(load_library(), name)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev).cuda_stream
+    elif isinstance(stream, torch.cuda.Stream):
+        if stream.device_index != dev:
+            raise ValueError(f"{name}: stream of cuda:{stream.device_index}, tensors on cuda:{dev}")
+        stream = stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, int(stream))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, int(stream))
+    if st != SVDQ_OK:
+        raise SVDQError(st, name)
+
+
+def svdq_pack_weight_i8(W_hat, K: int, N: int, Wq, sw, stream=None) -> None:
+    d = _cuda_index(W_hat, "W_hat")
+    _call("svdq_pack_weight_i8", d, stream, _vec(W_hat, torch.float32, K * N, d, "W_hat"), K, N,
+          _vec(Wq, torch.int8, N * K, d, "Wq"), _vec(sw, torch.float32, N, d, "sw"))
+
+
+def svdq_quantize_act_i8(X, M: int, K: int, inv_s, Xq, sx, stream=None) -> None:
+    d = _cuda_index(X, "X")
+    x, xt, ldx = _rows(X, M, K, d, "X")
+    _call("svdq_quantize_act_i8", d, stream, x, xt, ldx, M, K, _vec(inv_s, torch.float32, K, d, "inv_s"),
+          _vec(Xq, torch.int8, M * K, d, "Xq"), _vec(sx, torch.float32, M, d, "sx"))
+
+
+def svdq_linear_i8(Xq, sx, Wq, sw, bias, Y, M: int, N: int, K: int, stream=None) -> None:
+    d = _cuda_index(Xq, "Xq")
+    y, yt, ldy = _rows(Y, M, N, d, "Y")
+    _call("svdq_linear_i8", d, stream, _vec(Xq, torch.int8, M * K, d, "Xq"), _vec(sx, torch.float32, M, d, "sx"),
+          _vec(Wq, torch.int8, N * K, d, "Wq"), _vec(sw, torch.float32, N, d, "sw"),
+          _vec(bias, torch.float32, N, d, "bias"), y, yt, ldy, M, N, K)
+
+
+def svdq_forward_i8_workspace_bytes(M: int, K: int) -> int:
+    return int(load_library().svdq_forward_i8_workspace_bytes(M, K))
+
+
+def svdq_forward_i8(X, M: int, K: int, inv_s, Wq, sw, bias, Y, N: int, workspace, stream=None) -> None:
+    d = _cuda_index(X, "X")
+    x, xt, ldx = _rows(X, M, K, d, "X")
+    y, yt, ldy = _rows(Y, M, N, d, "Y")
+    _call("svdq_forward_i8", d, stream, x, xt, ldx, _vec(inv_s, torch.float32, K, d, "inv_s"),
+          _vec(Wq, torch.int8, N * K, d, "Wq"), _vec(sw, torch.float32, N, d, "sw"),
+          _vec(bias, torch.float32, N, d, "bias"), y, yt, ldy, M, N, K, _vec(workspace, torch.uint8, 0, d, "workspace"),
+          0 if workspace is None else workspace.numel())
+
+
+def svdq_group_norm_workspace_bytes(B: int, S: int, C: int, G: int) -> int:
+    return int(load_library().svdq_group_norm_workspace_bytes(B, S, C, G))
+
+
+def new_group_norm_workspace(B: int, S: int, C: int, G: int, device=None) -> Optional[torch.Tensor]:
+    """A zero-filled workspace for the group norms of this shape (None for a shape they refuse)."""
+    n = svdq_group_norm_workspace_bytes(B, S, C, G)
+    return torch.zeros(n, dtype=torch.uint8, device=device if device is not None else "cuda") if n else None
+
+
+def svdq_group_norm(X, B: int, S: int, C: int, G: int, gamma, beta, eps: float, act: int, Y, workspace,
+                    stream=None) -> None:
+    d = _cuda_index(X, "X")
+    x, xt, ldx = _rows(X, B * S, C, d, "X")
+    y, yt, ldy = _rows(Y, B * S, C, d, "Y")
+    if yt != xt:
+        raise TypeError(f"Y: expected dtype {X.dtype}, got {Y.dtype}")
+    _call("svdq_group_norm", d, stream, x, xt, ldx, B, S, C, G, _vec(gamma, torch.float32, C, d, "gamma"),
+          _vec(beta, torch.float32, C, d, "beta"), eps, act, y, ldy, _vec(workspace, torch.uint8, 0, d, "workspace"),
+          0 if workspace is None else workspace.numel())
+
+
+def svdq_group_norm_quantize_i8(X, B: int, S: int, C: int, G: int, gamma, beta, eps: float, act: int, inv_s, Xq, sx,
+                                workspace, stream=None) -> None:
+    d = _cuda_index(X, "X")
+    x, xt, ldx = _rows(X, B * S, C, d, "X")
+    _call("svdq_group_norm_quantize_i8", d, stream, x, xt, ldx, B, S, C, G, _vec(gamma, torch.float32, C, d, "gamma"),
+          _vec(beta, torch.float32, C, d, "beta"), eps, act, _vec(inv_s, torch.float32, C, d, "inv_s"),
+          _vec(Xq, torch.int8, B * S * C, d, "Xq"), _vec(sx, torch.float32, B * S, d, "sx"),
+          _vec(workspace, torch.uint8, 0, d, "workspace"), 0 if workspace is None else workspace.numel())
