@@ -153,6 +153,7 @@ __global__ void __launch_bounds__(256) k_quantize_act_i8(const T* __restrict__ X
                                                          float* __restrict__ sx) {
   __shared__ uint32_t part[8];
   griddep_wait();
+  griddep_launch_dependents();
   const int64_t m = blockIdx.x;
   const T* row = X + m * ldx;
   const int nv = K >> 3;

@@ -1,10 +1,16 @@
 // Int8 GEMM with scales per token and channel:
-//   Y[m, n] = f32(f32(f32(acc) sx[m]) sw[n]) + bias[n],  acc = sum_k Xq[m, k] Wq[n, k]  (int32, exact for K < 2^17)
-// rounded once to the type of Y.
+//   Y[m, n] = f32(f32(acc) sx[m]) sw[n] + bias[n],  acc = sum_k Xq[m, k] Wq[n, k]  (int32, exact for K < 2^17)
+// one fused multiply-add for the last product and the bias, rounded once to the type of Y.
+//
+// Both kernels run tcgen05.mma.kind::i8 on 128-byte chunks of K that TMA lands in 128-byte swizzled
+// tiles (chunks past K and rows past M or N are zero-filled and add nothing).
 #pragma once
 #include "int8.cuh"
+#include "tc_i8.cuh"
 
 namespace svdq {
+
+constexpr uint64_t L8_TIMEOUT_NS = 2000000000ull;
 
 struct LinearI8Args {
   const float* sx;
@@ -12,12 +18,21 @@ struct LinearI8Args {
   const float* bias;
   void* Y;
   int y_type;
+  int y_vec;            // Y's rows start on 16 bytes (32 where Y itself does): vector stores
   int64_t ldy;
   int M, N, K;
+  int nt;               // columns (pair kernel) or tokens (split kernel) of a tile
+  int stages;           // ring slots (split kernel)
+  int w_early;          // split kernel: the weight may be read before griddepcontrol.wait
 };
 
 SVDQ_DEV float i8_dequant(int acc, float sx, float sw, float bias) {
   return __fmaf_rn(__fmul_rn(__int2float_rn(acc), sx), sw, bias);
+}
+SVDQ_DEV uint32_t pack_16(float lo, float hi, int type) {
+  if (type == DT_BF16) return pack_bf16x2(lo, hi);
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 SVDQ_DEV void store_y(void* Y, int type, int64_t at, float y) {
   if (type == DT_BF16) static_cast<__nv_bfloat16*>(Y)[at] = __float2bfloat16_rn(y);
@@ -25,39 +40,420 @@ SVDQ_DEV void store_y(void* Y, int type, int64_t at, float y) {
   else static_cast<float*>(Y)[at] = y;
 }
 
-// 64 x 64 outputs a block, 4 x 4 a thread, four products an instruction.
-__global__ void __launch_bounds__(256) k_linear_i8(const int8_t* __restrict__ Xq, const int8_t* __restrict__ Wq,
-                                                   const LinearI8Args a) {
-  __shared__ uint32_t xs[64][17], ws[64][17];
-  griddep_wait();
-  const int m0 = blockIdx.x * 64, n0 = blockIdx.y * 64;
-  const int tm = threadIdx.x / 16, tn = threadIdx.x % 16;
-  int acc[4][4] = {};
-  for (int k0 = 0; k0 < a.K; k0 += 64) {
-    const int r = threadIdx.x / 4, c = (threadIdx.x % 4) * 16;
-    const bool kin = k0 + c < a.K;
-    const uint4 z = make_uint4(0, 0, 0, 0);
-    const uint4 x = kin && m0 + r < a.M ? *reinterpret_cast<const uint4*>(Xq + (int64_t)(m0 + r) * a.K + k0 + c) : z;
-    const uint4 w = kin && n0 + r < a.N ? *reinterpret_cast<const uint4*>(Wq + (int64_t)(n0 + r) * a.K + k0 + c) : z;
-    const int j = c / 4;
-    xs[r][j] = x.x; xs[r][j + 1] = x.y; xs[r][j + 2] = x.z; xs[r][j + 3] = x.w;
-    ws[r][j] = w.x; ws[r][j + 1] = w.y; ws[r][j + 2] = w.z; ws[r][j + 3] = w.w;
-    __syncthreads();
+// ------------------------------------------------------------------ pair kernel ---
+// Many tokens: persistent CTA pairs (one CTA an SM), tiles of 256 tokens x nt channels (nt 64..256), each
+// CTA holding 128 of the tokens and half of the channels' codes in a 6-slot ring of 32 KB, and the sums of
+// its 128 tokens in TMEM twice over (columns 0 and 256), so that a tile's epilogue runs under the next
+// tile's MMAs.  A pair's MMA reads each operand byte from shared memory half as often as two CTAs' own
+// would, and each CTA copies half of B.
+//   warp 0      copies (one thread): A and B boxes, both CTAs counting on the leader's barrier
+//   warp 1      leader only: MMAs (one thread);  in both: TMEM
+//   warps 4-11  epilogue: TMEM -> registers, scales and bias, stores (two warps a lane quarter)
+constexpr int LP_STAGES = 6;
+constexpr int LP_A_BYTES = 128 * 128;
+constexpr int LP_STAGE_BYTES = 2 * LP_A_BYTES;
+constexpr int LP_THREADS = 384;
+constexpr int LP_EPI_WARP0 = 4;
+constexpr int LP_EPI_WARPS = 8;
+constexpr int LP_STG_PITCH = 33;                                    // floats a row of a warp's staging tile
+constexpr int LP_STG_BYTES = 32 * LP_STG_PITCH * 4;
+constexpr int LP_OFF_STG = LP_STAGES * LP_STAGE_BYTES;
+constexpr int LP_OFF_BAR = LP_OFF_STG + LP_EPI_WARPS * LP_STG_BYTES;
+constexpr int LP_SMEM = LP_OFF_BAR + 256 + 1024;
+static_assert(LP_SMEM <= 232448, "shared memory of a CTA");
+
+#ifndef LP_RASTER
+#define LP_RASTER 8
+#endif
+// Tiles run in groups of LP_RASTER row blocks, the row block fastest: the pairs at work at one time
+// share few rows of X and few of Wq, which stay in L2.
+SVDQ_DEV void pair_tile(int t, int num_m, int num_n, int& mb, int& nb) {
+  const int per_group = LP_RASTER * num_n;
+  const int first = t / per_group * LP_RASTER;
+  const int gm = min(LP_RASTER, num_m - first);
+  const int w = t % per_group;
+  mb = first + w % gm;
+  nb = w / gm;
+}
+
+// 32 columns from n0 of one row a lane: rows row0 + lane (below a.M), values v.
+SVDQ_DEV void store_chunk(const LinearI8Args& a, const uint32_t (&v)[32], int row0, int n0, float sx, float* stg) {
+  const int lane = threadIdx.x & 31;
+  const int row = row0 + lane;
+  if (n0 >= a.N || row0 >= a.M) return;                             // warp-uniform
+  if (a.y_vec && n0 + 32 <= a.N) {
+    if (row >= a.M) return;
+    const float4* swp = reinterpret_cast<const float4*>(a.sw + n0);
+    const float4* bp = reinterpret_cast<const float4*>(a.bias + n0);
+    if (a.y_type == DT_FP32) {
+      float* dst = static_cast<float*>(a.Y) + (int64_t)row * a.ldy + n0;
 #pragma unroll
-    for (int k = 0; k < 16; ++k)
+      for (int i = 0; i < 8; ++i) {
+        const float4 s = __ldg(swp + i);
+        const float4 b = a.bias ? __ldg(bp + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+        reinterpret_cast<float4*>(dst)[i] =
+            make_float4(i8_dequant((int)v[4 * i], sx, s.x, b.x), i8_dequant((int)v[4 * i + 1], sx, s.y, b.y),
+                        i8_dequant((int)v[4 * i + 2], sx, s.z, b.z), i8_dequant((int)v[4 * i + 3], sx, s.w, b.w));
+      }
+    } else {
+      uint16_t* dst = static_cast<uint16_t*>(a.Y) + (int64_t)row * a.ldy + n0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int h = 0; h < 2; ++h) {
+        uint32_t o[8];
 #pragma unroll
-        for (int l = 0; l < 4; ++l) acc[i][l] = __dp4a((int)xs[tm * 4 + i][k], (int)ws[tn + 16 * l][k], acc[i][l]);
-    __syncthreads();
-  }
-  for (int i = 0; i < 4; ++i)
-    for (int l = 0; l < 4; ++l) {
-      const int m = m0 + tm * 4 + i, n = n0 + tn + 16 * l;
-      if (m < a.M && n < a.N)
-        store_y(a.Y, a.y_type, (int64_t)m * a.ldy + n,
-                i8_dequant(acc[i][l], __ldg(a.sx + m), __ldg(a.sw + n), a.bias ? __ldg(a.bias + n) : 0.0f));
+        for (int i = 0; i < 4; ++i) {
+          const int j = 4 * h + i;
+          const float4 s = __ldg(swp + j);
+          const float4 b = a.bias ? __ldg(bp + j) : make_float4(0.f, 0.f, 0.f, 0.f);
+          o[2 * i] = pack_16(i8_dequant((int)v[4 * j], sx, s.x, b.x), i8_dequant((int)v[4 * j + 1], sx, s.y, b.y),
+                             a.y_type);
+          o[2 * i + 1] = pack_16(i8_dequant((int)v[4 * j + 2], sx, s.z, b.z),
+                                 i8_dequant((int)v[4 * j + 3], sx, s.w, b.w), a.y_type);
+        }
+        if (a.y_vec == 2) {
+          st_global_v8(dst + 16 * h, o[0], o[1], o[2], o[3], o[4], o[5], o[6], o[7]);
+        } else {
+          reinterpret_cast<uint4*>(dst + 16 * h)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+          reinterpret_cast<uint4*>(dst + 16 * h)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+      }
     }
+    return;
+  }
+  // Ragged columns or rows at any alignment: through shared memory, a row's 32 columns by 32 lanes.
+#pragma unroll
+  for (int j = 0; j < 32; ++j) stg[lane * LP_STG_PITCH + j] = __fmul_rn(__int2float_rn((int)v[j]), sx);
+  __syncwarp();
+  const int n = n0 + lane;
+  if (n < a.N) {
+    const float s = __ldg(a.sw + n), b = a.bias ? __ldg(a.bias + n) : 0.0f;
+    const int rows = min(32, a.M - row0);
+    for (int i = 0; i < rows; ++i)
+      store_y(a.Y, a.y_type, (int64_t)(row0 + i) * a.ldy + n, __fmaf_rn(stg[i * LP_STG_PITCH + lane], s, b));
+  }
+  __syncwarp();
+}
+
+__global__ void __launch_bounds__(LP_THREADS, 1) k_linear_i8_pair(
+    const __grid_constant__ CUtensorMap tm_x,    // uint8 {K, M}, box {128, 128}, SW128
+    const __grid_constant__ CUtensorMap tm_w,    // uint8 {K, N}, box {128, nt / 2}, SW128
+    const LinearI8Args a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + LP_OFF_BAR);   // leader's: both CTAs' boxes landed
+  uint64_t* empty = full + LP_STAGES;                                 // own: slot consumed by the pair's MMAs
+  uint64_t* acc_full = empty + LP_STAGES;                             // own, per accumulator
+  uint64_t* acc_empty = acc_full + 2;                                 // leader's, per accumulator
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int nkt = (a.K + 127) >> 7;
+  const int num_m = (a.M + 255) >> 8, num_n = (a.N + a.nt - 1) / a.nt;
+  const int total = num_m * num_n, first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  const uint64_t tmo = L8_TIMEOUT_NS;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < LP_STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 2 * LP_EPI_WARPS);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_x);
+    tma_prefetch_desc(&tm_w);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync_all();                       // both CTAs' barriers and TMEM exist
+  tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  if (warp == 0 && lane == 0) {
+    // ------------------------------------------------------------------ copies ---
+    const uint32_t b_bytes = (uint32_t)(a.nt / 2) * 128u;
+    int it = 0;
+    bool ok = true;
+    for (int t = first; t < total && ok; t += step) {
+      int mb, nb;
+      pair_tile(t, num_m, num_n, mb, nb);
+      const int ya = mb * 256 + (int)rank * 128, yb = nb * a.nt + (int)rank * (a.nt / 2);
+      for (int kt = 0; kt < nkt; ++kt, ++it) {
+        const int s = it % LP_STAGES;
+        if (!mbar_wait_spin(&empty[s], (uint32_t)(((it / LP_STAGES) & 1) ^ 1), tmo, abort_flag, 0x501)) {
+          ok = false;
+          break;
+        }
+        const uint32_t bar = map_to_rank(smem_u32(&full[s]), 0);
+        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (LP_A_BYTES + b_bytes));
+        uint8_t* dst = smem + s * LP_STAGE_BYTES;
+        if (SVDQ_CHECK_OK(ya >= 0 && yb >= 0 && (uint32_t)(dst - smem_raw) + LP_STAGE_BYTES <= dyn_smem_bytes(), 0x5c1)) {
+          tma_load_2d_pair(dst, &tm_x, bar, kt * 128, ya);
+          tma_load_2d_pair(dst + LP_A_BYTES, &tm_w, bar, kt * 128, yb);
+        }
+      }
+    }
+    if (*abort_flag && rank == 0) {
+      // Give the copies in flight (both CTAs') the chance to land before the CTAs exit.
+      int never = 0;
+      for (int i = max(0, it - LP_STAGES); i < it; ++i)
+        mbar_wait(&full[i % LP_STAGES], (uint32_t)((i / LP_STAGES) & 1), tmo, &never, 0x502);
+    }
+  } else if (warp == 1 && lane == 0 && rank == 0) {
+    // -------------------------------------------------------------------- MMAs ---
+    const uint32_t idesc = idesc_i8(256, a.nt);
+    int s = 0, n = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int t = first; t < total && ok; t += step, ++n) {
+      const uint32_t d = tbase + 256u * (uint32_t)(n & 1);
+      if (n >= 2 && !mbar_wait_spin(&acc_empty[n & 1], (uint32_t)(((n >> 1) - 1) & 1), tmo, abort_flag, 0x511)) break;
+      tc_fence_after();
+      for (int kt = 0; kt < nkt; ++kt) {
+        if (!mbar_wait_spin(&full[s], phase, tmo, abort_flag, 0x512)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t base = smem_u32(smem + s * LP_STAGE_BYTES);
+        const uint64_t ad = sdesc_kmajor_sw128(base), bd = sdesc_kmajor_sw128(base + LP_A_BYTES);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) tc_mma_i8_pair(d, ad + 2 * j, bd + 2 * j, idesc, (kt | j) != 0 ? 1u : 0u);
+        tc_commit_pair(&empty[s]);
+        if (++s == LP_STAGES) { s = 0; phase ^= 1u; }
+      }
+      if (ok) tc_commit_pair(&acc_full[n & 1]);
+    }
+    if (*abort_flag) {
+      int never = 0;
+      tc_commit_pair(drain);
+      mbar_wait(drain, 0, tmo, &never, 0x513);
+    }
+  } else if (warp >= LP_EPI_WARP0) {
+    // ---------------------------------------------------------------- epilogue ---
+    const int ew = warp - LP_EPI_WARP0, q = warp & 3, h = ew >> 2;
+    float* stg = reinterpret_cast<float*>(smem + LP_OFF_STG + ew * LP_STG_BYTES);
+    const int chunks = a.nt >> 6;                        // 32-column chunks of this warp's half of the tile
+    int n = 0;
+    for (int t = first; t < total; t += step, ++n) {
+      int mb, nb;
+      pair_tile(t, num_m, num_n, mb, nb);
+      const int row0 = mb * 256 + (int)rank * 128 + 32 * q;
+      const float sx = row0 + lane < a.M ? __ldg(a.sx + row0 + lane) : 0.0f;
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(&acc_full[n & 1], (uint32_t)((n >> 1) & 1), tmo, abort_flag, 0x521))) break;
+      tc_fence_after();
+      const uint32_t ta = tbase + 256u * (uint32_t)(n & 1) + ((uint32_t)(32 * q) << 16) + (uint32_t)(h * (a.nt >> 1));
+      for (int c = 0; c < chunks; ++c) {
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(ta + 32 * c, v);
+        tmem_ld_wait();
+        reg_fence(v);
+        if (c == chunks - 1) {                           // all of this tile's sums are in registers: release it
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&acc_empty[n & 1]), 0));
+        }
+        store_chunk(a, v, row0, nb * a.nt + h * (a.nt >> 1) + 32 * c, sx, stg);
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync_all();                       // neither CTA leaves while the other may still reach it
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tbase, 512);
+  }
+}
+
+// ----------------------------------------------------------------- split kernel ---
+// Few tokens, where the weight's bytes count: the roles of the operands are swapped (A = 128 channels of
+// Wq, B = the tokens, nt of them), and the CTAs of a cluster share a tile's K axis, so that the GPU is
+// full whatever N is.  Each CTA streams its K range through a ring, leaves its integer sums in shared
+// memory, and after a cluster barrier sums a share of the tile's outputs over the cluster's CTAs (integers:
+// the order does not matter).
+//   warp 0  copies, warp 1 MMAs and TMEM (one thread each);  then all eight warps the epilogue
+constexpr int LS_THREADS = 256;
+constexpr int LS_A_BYTES = 128 * 128;
+constexpr int LS_BAR_BYTES = 256;
+
+__global__ void __launch_bounds__(LS_THREADS) k_linear_i8_split(
+    const __grid_constant__ CUtensorMap tm_w,    // uint8 {K, N}, box {128, 128}, SW128
+    const __grid_constant__ CUtensorMap tm_x,    // uint8 {K, M}, box {128, nt}, SW128
+    const LinearI8Args a, const int split) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int stage_bytes = LS_A_BYTES + a.nt * 128;
+  const int ring = max(a.stages * stage_bytes, a.nt * 512);            // the sums take the ring's place
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + ring);
+  uint64_t* empty = full + a.stages;
+  uint64_t* acc_full = empty + a.stages;
+  uint64_t* drain = acc_full + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = split > 1 ? (int)cluster_rank() : 0;
+  const int nb = blockIdx.x / split, mb = blockIdx.y;
+  const int nkt = (a.K + 127) >> 7;
+  const int k_lo = (int)((int64_t)nkt * rank / split), k_hi = (int)((int64_t)nkt * (rank + 1) / split);
+  const int nk = k_hi - k_lo;                                          // at least 1: split <= nkt
+  const uint32_t cols = a.nt <= 32 ? 32u : a.nt <= 64 ? 64u : a.nt <= 128 ? 128u : 256u;
+  const uint64_t tmo = L8_TIMEOUT_NS;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < a.stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(acc_full, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_w);
+    tma_prefetch_desc(&tm_x);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
+  int issued = 0;                                                      // copying thread: ring rounds begun
+
+  if (warp == 0 && lane == 0) {
+    const uint32_t x_bytes = (uint32_t)a.nt * 128u;
+    const int yw = nb * 128, yx = mb * a.nt;
+    const int ahead = a.w_early ? min(nk, a.stages) : 0;
+    // The weight's first boxes may come before the wait where the kernel launched just before this one has
+    // itself waited for all earlier work (svdq_forward_i8's quantizer): nothing in flight writes the weight.
+    for (int kt = 0; kt < ahead; ++kt) {
+      mbar_arrive_expect_tx(&full[kt], LS_A_BYTES + x_bytes);
+      uint8_t* dst = smem + kt * stage_bytes;
+      if (SVDQ_CHECK_OK((uint32_t)(dst - smem_raw) + stage_bytes <= dyn_smem_bytes(), 0x5c2))
+        tma_load_2d(dst, &tm_w, &full[kt], (k_lo + kt) * 128, yw);
+    }
+    issued = ahead;
+    griddep_wait();
+    for (int kt = 0; kt < nk; ++kt) {
+      const int s = kt % a.stages;
+      uint8_t* dst = smem + s * stage_bytes;
+      if (kt >= ahead) {
+        if (!mbar_wait_spin(&empty[s], (uint32_t)(((kt / a.stages) & 1) ^ 1), tmo, abort_flag, 0x531)) break;
+        mbar_arrive_expect_tx(&full[s], LS_A_BYTES + x_bytes);
+        if (SVDQ_CHECK_OK((uint32_t)(dst - smem_raw) + stage_bytes <= dyn_smem_bytes(), 0x5c3))
+          tma_load_2d(dst, &tm_w, &full[s], (k_lo + kt) * 128, yw);
+      }
+      if (SVDQ_CHECK_OK((uint32_t)(dst - smem_raw) + stage_bytes <= dyn_smem_bytes(), 0x5c4))
+        tma_load_2d(dst + LS_A_BYTES, &tm_x, &full[s], (k_lo + kt) * 128, yx);
+      issued = max(issued, kt + 1);
+    }
+  } else if (warp == 1 && lane == 0) {
+    const uint32_t idesc = idesc_i8(128, a.nt);
+    int kt = 0;
+    for (; kt < nk; ++kt) {
+      const int s = kt % a.stages;
+      if (!mbar_wait_spin(&full[s], (uint32_t)((kt / a.stages) & 1), tmo, abort_flag, 0x532)) break;
+      tc_fence_after();
+      const uint32_t base = smem_u32(smem + s * stage_bytes);
+      const uint64_t ad = sdesc_kmajor_sw128(base), bd = sdesc_kmajor_sw128(base + LS_A_BYTES);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) tc_mma_i8(tbase, ad + 2 * j, bd + 2 * j, idesc, (kt | j) != 0 ? 1u : 0u);
+      if (kt + a.stages < nk) tc_commit(&empty[s]);      // nobody waits for the last round of slots
+    }
+    tc_commit(kt == nk ? acc_full : drain);
+    if (kt < nk) {
+      int never = 0;
+      mbar_wait(drain, 0, tmo, &never, 0x534);
+    }
+  }
+  __syncwarp();
+
+  // ------------------------------------------------------------------ epilogue ---
+  if (warp != 0 || lane != 0) griddep_wait();            // the copying thread has waited
+  __syncwarp();
+  griddep_launch_dependents();
+  const bool got = __all_sync(0xFFFFFFFFu, mbar_wait(acc_full, 0, tmo, abort_flag, 0x533));
+  if (!got && warp == 0 && lane == 0) {                  // let the copies in flight land before the CTA exits
+    int never = 0;
+    for (int kt = max(0, issued - a.stages); kt < issued; ++kt)
+      mbar_wait(&full[kt % a.stages], (uint32_t)((kt / a.stages) & 1), tmo, &never, 0x535);
+  }
+  __syncwarp();
+  tc_fence_after();
+  // Every copy has landed and every MMA is done: the ring holds the sums now, nt rows (tokens) of 128 channels.
+  int* part = reinterpret_cast<int*>(smem);
+  const int q = warp & 3;
+  if (got) {
+    for (int c0 = 16 * (warp >> 2); c0 < a.nt; c0 += 32) {
+      uint32_t v[16];
+      tmem_ld_32x32b_x16(tbase + ((uint32_t)(32 * q) << 16) + (uint32_t)c0, v);
+      tmem_ld_wait();
+      reg_fence16(v);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) part[(c0 + j) * 128 + 32 * q + lane] = (int)v[j];
+    }
+  }
+  tc_fence_before();
+  if (split > 1) cluster_sync_all();
+  else __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tbase, cols);
+  }
+  const int tokens = min(a.nt, a.M - mb * a.nt);
+  const int n = nb * 128 + 4 * lane;                     // four channels a lane
+  float s4[4], b4[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    s4[i] = n + i < a.N ? __ldg(a.sw + n + i) : 0.0f;
+    b4[i] = a.bias && n + i < a.N ? __ldg(a.bias + n + i) : 0.0f;
+  }
+  const uint32_t mine = smem_u32(part) + 16u * (uint32_t)lane;
+  for (int t = rank + split * warp; t < tokens; t += split * (LS_THREADS / 32)) {
+    int4 acc = make_int4(0, 0, 0, 0);
+    for (int r = 0; r < split; ++r) {
+      const int4 v = ld_cluster_v4(split > 1 ? map_to_rank(mine + 512u * (uint32_t)t, (uint32_t)r) : mine + 512u * (uint32_t)t);
+      acc.x += v.x;
+      acc.y += v.y;
+      acc.z += v.z;
+      acc.w += v.w;
+    }
+    const int row = mb * a.nt + t;
+    const float sx = __ldg(a.sx + row);
+    const float y0 = i8_dequant(acc.x, sx, s4[0], b4[0]), y1 = i8_dequant(acc.y, sx, s4[1], b4[1]);
+    const float y2 = i8_dequant(acc.z, sx, s4[2], b4[2]), y3 = i8_dequant(acc.w, sx, s4[3], b4[3]);
+    const int64_t at = (int64_t)row * a.ldy + n;
+    if (a.y_vec && n + 4 <= a.N) {
+      if (a.y_type == DT_FP32)
+        *reinterpret_cast<float4*>(static_cast<float*>(a.Y) + at) = make_float4(y0, y1, y2, y3);
+      else
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.Y) + at) =
+            make_uint2(pack_16(y0, y1, a.y_type), pack_16(y2, y3, a.y_type));
+    } else {
+      if (n < a.N) store_y(a.Y, a.y_type, at, y0);
+      if (n + 1 < a.N) store_y(a.Y, a.y_type, at + 1, y1);
+      if (n + 2 < a.N) store_y(a.Y, a.y_type, at + 2, y2);
+      if (n + 3 < a.N) store_y(a.Y, a.y_type, at + 3, y3);
+    }
+  }
+  __syncwarp();
+  if (split > 1) cluster_sync_all();                     // no CTA leaves while another reads its sums
 }
 
 }  // namespace svdq

@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -480,22 +481,85 @@ svdq_status launch_quantize_i8(const void* X, int x_type, int64_t ldx, int64_t M
   return e == cudaSuccess ? launch_status() : SVDQ_ERR_CUDA;
 }
 
-svdq_status launch_linear_i8(DevInfo* d, const int8_t* Xq, const float* sx, const int8_t* Wq, const float* sw,
-                             const float* bias, void* Y, int y_type, int64_t ldy, int64_t M, int64_t N, int64_t K,
-                             cudaStream_t s) {
-  (void)d;
+// Shared memory a kernel may use, raised once per device and kernel.
+template <typename F>
+svdq_status allow_smem(F kernel, int dev, std::atomic<bool> (&done)[kMaxDevices], int bytes) {
+  if (done[dev].load(std::memory_order_acquire)) return SVDQ_OK;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    return SVDQ_ERR_CUDA;
+  done[dev].store(true, std::memory_order_release);
+  return SVDQ_OK;
+}
+
+int y_vector(const void* Y, int type, int64_t ldy) {
+  const uint64_t pitch = (uint64_t)ldy * dtype_size(type);
+  if (pitch % 16 != 0) return 0;
+  return pitch % 32 == 0 && (reinterpret_cast<uintptr_t>(Y) & 31u) == 0 ? 2 : 1;
+}
+
+std::atomic<bool> g_pair_attr[kMaxDevices], g_split_attr[kMaxDevices];
+
+// w_early: the kernel before this one on the stream is a quantizer of this library, which has waited for
+// everything before it, so the weight may be read while it still runs.
+svdq_status launch_linear_i8(int dev, DevInfo* d, const int8_t* Xq, const float* sx, const int8_t* Wq,
+                             const float* sw, const float* bias, void* Y, int y_type, int64_t ldy, int64_t M,
+                             int64_t N, int64_t K, int w_early, cudaStream_t s) {
   LinearI8Args a;
   a.sx = sx;
   a.sw = sw;
   a.bias = bias;
   a.Y = Y;
   a.y_type = y_type;
+  a.y_vec = y_vector(Y, y_type, ldy);
   a.ldy = ldy;
   a.M = (int)M;
   a.N = (int)N;
   a.K = (int)K;
-  const dim3 grid((unsigned)((M + 63) / 64), (unsigned)((N + 63) / 64));
-  if (launch_pdl(k_linear_i8, grid, dim3(256), 0, s, 1, Xq, Wq, a) != cudaSuccess) return SVDQ_ERR_CUDA;
+  a.w_early = w_early;
+  a.stages = 0;
+  svdq_status st;
+  const int nkt = (int)((K + 127) / 128);
+  CUtensorMap tm_x, tm_w;
+  if (M <= 256) {
+    a.nt = (int)((M + 15) / 16 * 16);
+    const int stage = LS_A_BYTES + a.nt * 128;
+    const int budget = a.nt <= 128 ? 100 * 1024 : 200 * 1024;
+    const int slots = d->sms * (a.nt <= 128 ? 2 : 1);
+    const int tiles = (int)((N + 127) / 128);
+    int split = 1;
+    while (split < 8 && (int64_t)tiles * (split + 1) <= slots && nkt >= 2 * (split + 1)) ++split;
+    const int per = (nkt + split - 1) / split;
+    a.stages = std::max(1, std::min(std::min(per, budget / stage), 12));
+    const size_t smem = (size_t)std::max(a.stages * stage, a.nt * 512) + LS_BAR_BYTES + 1024;
+    if (!make_map_2d(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, Wq, (uint64_t)K, (uint64_t)N, (uint64_t)K, 128, 128) ||
+        !make_map_2d(&tm_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, Xq, (uint64_t)K, (uint64_t)M, (uint64_t)K, 128,
+                     (uint32_t)a.nt))
+      return SVDQ_ERR_CUDA;
+    if ((st = allow_smem(k_linear_i8_split, dev, g_split_attr, 200 * 1024 + LS_BAR_BYTES + 1024)) != SVDQ_OK) return st;
+    if (launch_pdl(k_linear_i8_split, dim3((unsigned)(tiles * split)), dim3(LS_THREADS), smem, s, split, tm_w, tm_x, a,
+                   split) != cudaSuccess)
+      return SVDQ_ERR_CUDA;
+    return launch_status();
+  }
+  const int64_t num_m = (M + 255) / 256, pairs = d->sms / 2;
+  int64_t best = 0;
+  for (int nt = 256; nt >= 64; nt -= 64) {       // waves of tiles, a tile costing its columns and a fixed part
+    const int64_t cost = (num_m * ((N + nt - 1) / nt) + pairs - 1) / pairs * (nt + 24);
+    if (nt == 256 || cost < best) {
+      best = cost;
+      a.nt = nt;
+    }
+  }
+  if (!make_map_2d(&tm_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, Xq, (uint64_t)K, (uint64_t)M, (uint64_t)K, 128, 128) ||
+      !make_map_2d(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, Wq, (uint64_t)K, (uint64_t)N, (uint64_t)K, 128,
+                   (uint32_t)(a.nt / 2)))
+    return SVDQ_ERR_CUDA;
+  if ((st = allow_smem(k_linear_i8_pair, dev, g_pair_attr, LP_SMEM)) != SVDQ_OK) return st;
+  const int64_t tiles = num_m * ((N + a.nt - 1) / a.nt);
+  if (tiles > kMaxDim) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+  if (launch_pdl(k_linear_i8_pair, dim3((unsigned)(2 * std::min(tiles, pairs))), dim3(LP_THREADS), (size_t)LP_SMEM, s, 2,
+                 tm_x, tm_w, a) != cudaSuccess)
+    return SVDQ_ERR_CUDA;
   return launch_status();
 }
 
@@ -756,7 +820,8 @@ svdq_status svdq_linear_i8(const int8_t* Xq, const float* sx, const int8_t* Wq, 
   int dev;
   DevInfo* d;
   if ((st = current_device(&dev, &d)) != SVDQ_OK) return st;
-  return launch_linear_i8(d, Xq, sx, Wq, sw, bias, Y, y_type, ldy, M, N, K, reinterpret_cast<cudaStream_t>(stream));
+  return launch_linear_i8(dev, d, Xq, sx, Wq, sw, bias, Y, y_type, ldy, M, N, K, 0,
+                          reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t svdq_forward_i8_workspace_bytes(int64_t M, int64_t K) {
@@ -784,7 +849,7 @@ svdq_status svdq_forward_i8(const void* X, int x_type, int64_t ldx, const float*
   int8_t* Xq = static_cast<int8_t*>(workspace);           // M x K codes (K % 16 == 0), then the M scales
   float* sx = reinterpret_cast<float*>(Xq + (size_t)M * (size_t)K);
   if ((st = launch_quantize_i8(X, x_type, ldx, M, K, inv_s, Xq, sx, s)) != SVDQ_OK) return st;
-  return launch_linear_i8(d, Xq, sx, Wq, sw, bias, Y, y_type, ldy, M, N, K, s);
+  return launch_linear_i8(dev, d, Xq, sx, Wq, sw, bias, Y, y_type, ldy, M, N, K, 1, s);
 }
 
 size_t svdq_group_norm_workspace_bytes(int64_t B, int64_t S, int64_t C, int64_t G) {
