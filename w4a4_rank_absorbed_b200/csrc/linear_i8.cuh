@@ -18,7 +18,7 @@ struct LinearI8Args {
   const float* bias;
   void* Y;
   int y_type;
-  int y_vec;            // Y's rows start on 16 bytes (32 where Y itself does): vector stores
+  int y_vec;            // Y's rows start on 16 bytes (2: on 32): vector stores
   int64_t ldy;
   int M, N, K;
   int nt;               // columns (pair kernel) or tokens (split kernel) of a tile
@@ -55,8 +55,7 @@ constexpr int LP_STAGE_BYTES = 2 * LP_A_BYTES;
 constexpr int LP_THREADS = 384;
 constexpr int LP_EPI_WARP0 = 4;
 constexpr int LP_EPI_WARPS = 8;
-constexpr int LP_STG_PITCH = 33;                                    // floats a row of a warp's staging tile
-constexpr int LP_STG_BYTES = 32 * LP_STG_PITCH * 4;
+constexpr int LP_STG_BYTES = 2048 + 1024;        // a warp's 16 x 32 staging tile; its 128 channels' scales and biases
 constexpr int LP_OFF_STG = LP_STAGES * LP_STAGE_BYTES;
 constexpr int LP_OFF_BAR = LP_OFF_STG + LP_EPI_WARPS * LP_STG_BYTES;
 constexpr int LP_SMEM = LP_OFF_BAR + 256 + 1024;
@@ -76,62 +75,66 @@ SVDQ_DEV void pair_tile(int t, int num_m, int num_n, int& mb, int& nb) {
   nb = w / gm;
 }
 
-// 32 columns from n0 of one row a lane: rows row0 + lane (below a.M), values v.
-SVDQ_DEV void store_chunk(const LinearI8Args& a, const uint32_t (&v)[32], int row0, int n0, float sx, float* stg) {
+// 32 columns from n0 of one row a lane: rows row0 + lane (below a.M), sums v.  chan: the columns' scales, and
+// 512 bytes on their biases, in shared memory.
+SVDQ_DEV void store_chunk(const LinearI8Args& a, const uint32_t (&v)[32], int row0, int n0, float sx, uint32_t chan,
+                          float* stg) {
   const int lane = threadIdx.x & 31;
   const int row = row0 + lane;
   if (n0 >= a.N || row0 >= a.M) return;                             // warp-uniform
   if (a.y_vec && n0 + 32 <= a.N) {
-    if (row >= a.M) return;
-    const float4* swp = reinterpret_cast<const float4*>(a.sw + n0);
-    const float4* bp = reinterpret_cast<const float4*>(a.bias + n0);
-    if (a.y_type == DT_FP32) {
-      float* dst = static_cast<float*>(a.Y) + (int64_t)row * a.ldy + n0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 s = __ldg(swp + i);
-        const float4 b = a.bias ? __ldg(bp + i) : make_float4(0.f, 0.f, 0.f, 0.f);
-        reinterpret_cast<float4*>(dst)[i] =
-            make_float4(i8_dequant((int)v[4 * i], sx, s.x, b.x), i8_dequant((int)v[4 * i + 1], sx, s.y, b.y),
-                        i8_dequant((int)v[4 * i + 2], sx, s.z, b.z), i8_dequant((int)v[4 * i + 3], sx, s.w, b.w));
+    for (int h = 0; h < 2; ++h) {
+      float y[16];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 s = lds_v4(chan + 64 * h + 16 * i), b = lds_v4(chan + 512 + 64 * h + 16 * i);
+        const int j = 16 * h + 4 * i;
+        y[4 * i] = i8_dequant((int)v[j], sx, __uint_as_float(s.x), __uint_as_float(b.x));
+        y[4 * i + 1] = i8_dequant((int)v[j + 1], sx, __uint_as_float(s.y), __uint_as_float(b.y));
+        y[4 * i + 2] = i8_dequant((int)v[j + 2], sx, __uint_as_float(s.z), __uint_as_float(b.z));
+        y[4 * i + 3] = i8_dequant((int)v[j + 3], sx, __uint_as_float(s.w), __uint_as_float(b.w));
       }
-    } else {
-      uint16_t* dst = static_cast<uint16_t*>(a.Y) + (int64_t)row * a.ldy + n0;
+      if (row >= a.M) continue;
+      const int64_t at = (int64_t)row * a.ldy + n0 + 16 * h;
+      if (a.y_type == DT_FP32) {
+        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.Y) + at);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+        for (int i = 0; i < 4; ++i) dst[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+      } else {
         uint32_t o[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int j = 4 * h + i;
-          const float4 s = __ldg(swp + j);
-          const float4 b = a.bias ? __ldg(bp + j) : make_float4(0.f, 0.f, 0.f, 0.f);
-          o[2 * i] = pack_16(i8_dequant((int)v[4 * j], sx, s.x, b.x), i8_dequant((int)v[4 * j + 1], sx, s.y, b.y),
-                             a.y_type);
-          o[2 * i + 1] = pack_16(i8_dequant((int)v[4 * j + 2], sx, s.z, b.z),
-                                 i8_dequant((int)v[4 * j + 3], sx, s.w, b.w), a.y_type);
-        }
+        for (int i = 0; i < 8; ++i) o[i] = pack_16(y[2 * i], y[2 * i + 1], a.y_type);
+        uint16_t* dst = static_cast<uint16_t*>(a.Y) + at;
         if (a.y_vec == 2) {
-          st_global_v8(dst + 16 * h, o[0], o[1], o[2], o[3], o[4], o[5], o[6], o[7]);
+          st_global_v8(dst, o[0], o[1], o[2], o[3], o[4], o[5], o[6], o[7]);
         } else {
-          reinterpret_cast<uint4*>(dst + 16 * h)[0] = make_uint4(o[0], o[1], o[2], o[3]);
-          reinterpret_cast<uint4*>(dst + 16 * h)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+          reinterpret_cast<uint4*>(dst)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+          reinterpret_cast<uint4*>(dst)[1] = make_uint4(o[4], o[5], o[6], o[7]);
         }
       }
     }
     return;
   }
-  // Ragged columns or rows at any alignment: through shared memory, a row's 32 columns by 32 lanes.
-#pragma unroll
-  for (int j = 0; j < 32; ++j) stg[lane * LP_STG_PITCH + j] = __fmul_rn(__int2float_rn((int)v[j]), sx);
-  __syncwarp();
+  // Ragged columns or rows at any alignment: 16 rows at a time are turned in the warp's staging buffer (element
+  // (r, c) at 32 r + (c ^ r): no bank conflict either way), and 32 lanes store a row's 32 columns.
   const int n = n0 + lane;
-  if (n < a.N) {
-    const float s = __ldg(a.sw + n), b = a.bias ? __ldg(a.bias + n) : 0.0f;
-    const int rows = min(32, a.M - row0);
-    for (int i = 0; i < rows; ++i)
-      store_y(a.Y, a.y_type, (int64_t)(row0 + i) * a.ldy + n, __fmaf_rn(stg[i * LP_STG_PITCH + lane], s, b));
+  const float s = lds_f32(chan + 4 * lane), b = lds_f32(chan + 512 + 4 * lane);
+#pragma unroll 1
+  for (int g = 0; g < 32; g += 16) {
+    __syncwarp();
+    if ((lane & 16) == g) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) stg[(lane & 15) * 32 + (j ^ (lane & 15))] = __fmul_rn(__int2float_rn((int)v[j]), sx);
+    }
+    __syncwarp();
+    const int rows = min(16, a.M - row0 - g);
+    if (n < a.N) {
+#pragma unroll 4
+      for (int i = 0; i < rows; ++i)
+        store_y(a.Y, a.y_type, (int64_t)(row0 + g + i) * a.ldy + n, __fmaf_rn(stg[i * 32 + (lane ^ i)], s, b));
+    }
   }
-  __syncwarp();
 }
 
 __global__ void __launch_bounds__(LP_THREADS, 1) k_linear_i8_pair(
@@ -148,8 +151,8 @@ __global__ void __launch_bounds__(LP_THREADS, 1) k_linear_i8_pair(
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank();
+  const int warp = (int)warp_uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const uint32_t rank = warp_uniform(cluster_rank());
   const int nkt = (a.K + 127) >> 7;
   const int num_m = (a.M + 255) >> 8, num_n = (a.N + a.nt - 1) / a.nt;
   const int total = num_m * num_n, first = blockIdx.x >> 1, step = gridDim.x >> 1;
@@ -178,81 +181,120 @@ __global__ void __launch_bounds__(LP_THREADS, 1) k_linear_i8_pair(
   tc_fence_before();
   cluster_sync_all();                       // both CTAs' barriers and TMEM exist
   tc_fence_after();
-  const uint32_t tbase = *tmem_slot;
+  const uint32_t tbase = warp_uniform(*tmem_slot);
+  const uint32_t full0 = warp_uniform(map_to_rank(smem_u32(full), 0));
   griddep_wait();
   griddep_launch_dependents();
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
     // ------------------------------------------------------------------ copies ---
-    const uint32_t b_bytes = (uint32_t)(a.nt / 2) * 128u;
-    int it = 0;
+    const uint32_t bytes = 2 * (LP_A_BYTES + (uint32_t)(a.nt / 2) * 128u);   // of both CTAs
+    int s = 0, issued = 0;
+    uint32_t phase = 1;
     bool ok = true;
     for (int t = first; t < total && ok; t += step) {
       int mb, nb;
       pair_tile(t, num_m, num_n, mb, nb);
       const int ya = mb * 256 + (int)rank * 128, yb = nb * a.nt + (int)rank * (a.nt / 2);
-      for (int kt = 0; kt < nkt; ++kt, ++it) {
-        const int s = it % LP_STAGES;
-        if (!mbar_wait_spin(&empty[s], (uint32_t)(((it / LP_STAGES) & 1) ^ 1), tmo, abort_flag, 0x501)) {
+      for (int kt = 0; kt < nkt; ++kt) {
+        if (!mbar_wait_warp(&empty[s], phase, tmo, abort_flag, 0x501)) {
           ok = false;
           break;
         }
-        const uint32_t bar = map_to_rank(smem_u32(&full[s]), 0);
-        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (LP_A_BYTES + b_bytes));
         uint8_t* dst = smem + s * LP_STAGE_BYTES;
-        if (SVDQ_CHECK_OK(ya >= 0 && yb >= 0 && (uint32_t)(dst - smem_raw) + LP_STAGE_BYTES <= dyn_smem_bytes(), 0x5c1)) {
-          tma_load_2d_pair(dst, &tm_x, bar, kt * 128, ya);
-          tma_load_2d_pair(dst + LP_A_BYTES, &tm_w, bar, kt * 128, yb);
+        const uint32_t bar = full0 + 8u * (uint32_t)s;
+        if (elect_one()) {
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
+          if (SVDQ_CHECK_OK(ya >= 0 && yb >= 0 && (uint32_t)(dst - smem_raw) + LP_STAGE_BYTES <= dyn_smem_bytes(), 0x5c1)) {
+            tma_load_2d_pair(dst, &tm_x, bar, kt * 128, ya);
+            tma_load_2d_pair(dst + LP_A_BYTES, &tm_w, bar, kt * 128, yb);
+          }
+        }
+        __syncwarp();
+        ++issued;
+        if (++s == LP_STAGES) {
+          s = 0;
+          phase ^= 1u;
         }
       }
     }
-    if (*abort_flag && rank == 0) {
+    if (*abort_flag && rank == 0 && lane == 0) {
       // Give the copies in flight (both CTAs') the chance to land before the CTAs exit.
       int never = 0;
-      for (int i = max(0, it - LP_STAGES); i < it; ++i)
+      for (int i = max(0, issued - LP_STAGES); i < issued; ++i)
         mbar_wait(&full[i % LP_STAGES], (uint32_t)((i / LP_STAGES) & 1), tmo, &never, 0x502);
     }
-  } else if (warp == 1 && lane == 0 && rank == 0) {
+  } else if (warp == 1 && rank == 0) {
     // -------------------------------------------------------------------- MMAs ---
     const uint32_t idesc = idesc_i8(256, a.nt);
+    const uint64_t desc0 = sdesc_kmajor_sw128(smem_u32(smem));
     int s = 0, n = 0;
     uint32_t phase = 0;
     bool ok = true;
     for (int t = first; t < total && ok; t += step, ++n) {
       const uint32_t d = tbase + 256u * (uint32_t)(n & 1);
-      if (n >= 2 && !mbar_wait_spin(&acc_empty[n & 1], (uint32_t)(((n >> 1) - 1) & 1), tmo, abort_flag, 0x511)) break;
+      if (n >= 2 && !mbar_wait_warp(&acc_empty[n & 1], (uint32_t)(((n >> 1) - 1) & 1), tmo, abort_flag, 0x511)) break;
       tc_fence_after();
       for (int kt = 0; kt < nkt; ++kt) {
-        if (!mbar_wait_spin(&full[s], phase, tmo, abort_flag, 0x512)) {
+        if (!mbar_wait_warp(&full[s], phase, tmo, abort_flag, 0x512)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t base = smem_u32(smem + s * LP_STAGE_BYTES);
-        const uint64_t ad = sdesc_kmajor_sw128(base), bd = sdesc_kmajor_sw128(base + LP_A_BYTES);
+        const uint64_t ad = desc0 + (uint64_t)(s * (LP_STAGE_BYTES / 16)), bd = ad + LP_A_BYTES / 16;
+        if (elect_one()) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) tc_mma_i8_pair(d, ad + 2 * j, bd + 2 * j, idesc, (kt | j) != 0 ? 1u : 0u);
-        tc_commit_pair(&empty[s]);
-        if (++s == LP_STAGES) { s = 0; phase ^= 1u; }
+          for (int j = 0; j < 4; ++j) tc_mma_i8_pair(d, ad + 2 * j, bd + 2 * j, idesc, (kt | j) != 0 ? 1u : 0u);
+          tc_commit_pair(&empty[s]);
+          if (kt == nkt - 1) tc_commit_pair(&acc_full[n & 1]);
+        }
+        __syncwarp();
+        if (++s == LP_STAGES) {
+          s = 0;
+          phase ^= 1u;
+        }
       }
-      if (ok) tc_commit_pair(&acc_full[n & 1]);
     }
     if (*abort_flag) {
       int never = 0;
-      tc_commit_pair(drain);
+      if (elect_one()) tc_commit_pair(drain);
+      __syncwarp();
       mbar_wait(drain, 0, tmo, &never, 0x513);
     }
   } else if (warp >= LP_EPI_WARP0) {
     // ---------------------------------------------------------------- epilogue ---
     const int ew = warp - LP_EPI_WARP0, q = warp & 3, h = ew >> 2;
     float* stg = reinterpret_cast<float*>(smem + LP_OFF_STG + ew * LP_STG_BYTES);
+    float* chan = stg + 512;
     const int chunks = a.nt >> 6;                        // 32-column chunks of this warp's half of the tile
     int n = 0;
     for (int t = first; t < total; t += step, ++n) {
       int mb, nb;
       pair_tile(t, num_m, num_n, mb, nb);
-      const int row0 = mb * 256 + (int)rank * 128 + 32 * q;
+      const int row0 = mb * 256 + (int)rank * 128 + 32 * q, col0 = nb * a.nt + h * (a.nt >> 1);
       const float sx = row0 + lane < a.M ? __ldg(a.sx + row0 + lane) : 0.0f;
+      __syncwarp();                                      // the last tile's reads of them are done
+      // the tile's channel scales and biases, while the sums are on their way
+      if (4 * lane < (a.nt >> 1)) {
+        const int c = col0 + 4 * lane;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f), b = s;
+        if (c + 4 <= a.N) {
+          s = __ldg(reinterpret_cast<const float4*>(a.sw + c));
+          if (a.bias) b = __ldg(reinterpret_cast<const float4*>(a.bias + c));
+        } else {
+          float* sv = reinterpret_cast<float*>(&s);
+          float* bv = reinterpret_cast<float*>(&b);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (c + i < a.N) {
+              sv[i] = __ldg(a.sw + c + i);
+              if (a.bias) bv[i] = __ldg(a.bias + c + i);
+            }
+        }
+        *reinterpret_cast<float4*>(chan + 4 * lane) = s;
+        *reinterpret_cast<float4*>(chan + 128 + 4 * lane) = b;
+      }
+      __syncwarp();
       if (!__all_sync(0xFFFFFFFFu, mbar_wait(&acc_full[n & 1], (uint32_t)((n >> 1) & 1), tmo, abort_flag, 0x521))) break;
       tc_fence_after();
       const uint32_t ta = tbase + 256u * (uint32_t)(n & 1) + ((uint32_t)(32 * q) << 16) + (uint32_t)(h * (a.nt >> 1));
@@ -266,7 +308,7 @@ __global__ void __launch_bounds__(LP_THREADS, 1) k_linear_i8_pair(
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&acc_empty[n & 1]), 0));
         }
-        store_chunk(a, v, row0, nb * a.nt + h * (a.nt >> 1) + 32 * c, sx, stg);
+        store_chunk(a, v, row0, col0 + 32 * c, sx, smem_u32(chan) + 128u * (uint32_t)c, stg);
       }
     }
   }
@@ -288,7 +330,7 @@ __global__ void __launch_bounds__(LP_THREADS, 1) k_linear_i8_pair(
 //   warp 0  copies, warp 1 MMAs and TMEM (one thread each);  then all eight warps the epilogue
 constexpr int LS_THREADS = 256;
 constexpr int LS_A_BYTES = 128 * 128;
-constexpr int LS_BAR_BYTES = 256;
+constexpr int LS_TAIL_BYTES = 256 + 1024;                 // barriers, then the tile's token scales
 
 __global__ void __launch_bounds__(LS_THREADS) k_linear_i8_split(
     const __grid_constant__ CUtensorMap tm_w,    // uint8 {K, N}, box {128, 128}, SW128
@@ -304,9 +346,10 @@ __global__ void __launch_bounds__(LS_THREADS) k_linear_i8_split(
   uint64_t* drain = acc_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* sxs = reinterpret_cast<float*>(smem + ring + 256);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = split > 1 ? (int)cluster_rank() : 0;
+  const int warp = (int)warp_uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int rank = split > 1 ? (int)warp_uniform(cluster_rank()) : 0;
   const int nb = blockIdx.x / split, mb = blockIdx.y;
   const int nkt = (a.K + 127) >> 7;
   const int k_lo = (int)((int64_t)nkt * rank / split), k_hi = (int)((int64_t)nkt * (rank + 1) / split);
@@ -333,61 +376,87 @@ __global__ void __launch_bounds__(LS_THREADS) k_linear_i8_split(
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tbase = *tmem_slot;
-  int issued = 0;                                                      // copying thread: ring rounds begun
+  const uint32_t tbase = warp_uniform(*tmem_slot);
+  int issued = 0;                                                      // copying warp: ring rounds begun
 
-  if (warp == 0 && lane == 0) {
-    const uint32_t x_bytes = (uint32_t)a.nt * 128u;
+  if (warp == 0) {
     const int yw = nb * 128, yx = mb * a.nt;
     const int ahead = a.w_early ? min(nk, a.stages) : 0;
     // The weight's first boxes may come before the wait where the kernel launched just before this one has
     // itself waited for all earlier work (svdq_forward_i8's quantizer): nothing in flight writes the weight.
     for (int kt = 0; kt < ahead; ++kt) {
-      mbar_arrive_expect_tx(&full[kt], LS_A_BYTES + x_bytes);
       uint8_t* dst = smem + kt * stage_bytes;
-      if (SVDQ_CHECK_OK((uint32_t)(dst - smem_raw) + stage_bytes <= dyn_smem_bytes(), 0x5c2))
-        tma_load_2d(dst, &tm_w, &full[kt], (k_lo + kt) * 128, yw);
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&full[kt], (uint32_t)stage_bytes);
+        if (SVDQ_CHECK_OK((uint32_t)(dst - smem_raw) + stage_bytes <= dyn_smem_bytes(), 0x5c2))
+          tma_load_2d(dst, &tm_w, &full[kt], (k_lo + kt) * 128, yw);
+      }
+      __syncwarp();
     }
     issued = ahead;
     griddep_wait();
+    int s = 0;
+    uint32_t phase = 1;
     for (int kt = 0; kt < nk; ++kt) {
-      const int s = kt % a.stages;
       uint8_t* dst = smem + s * stage_bytes;
-      if (kt >= ahead) {
-        if (!mbar_wait_spin(&empty[s], (uint32_t)(((kt / a.stages) & 1) ^ 1), tmo, abort_flag, 0x531)) break;
-        mbar_arrive_expect_tx(&full[s], LS_A_BYTES + x_bytes);
-        if (SVDQ_CHECK_OK((uint32_t)(dst - smem_raw) + stage_bytes <= dyn_smem_bytes(), 0x5c3))
-          tma_load_2d(dst, &tm_w, &full[s], (k_lo + kt) * 128, yw);
+      if (kt >= ahead && !mbar_wait_warp(&empty[s], phase, tmo, abort_flag, 0x531)) break;
+      if (elect_one()) {
+        if (kt >= ahead) mbar_arrive_expect_tx(&full[s], (uint32_t)stage_bytes);
+        if (SVDQ_CHECK_OK((uint32_t)(dst - smem_raw) + stage_bytes <= dyn_smem_bytes(), 0x5c3)) {
+          if (kt >= ahead) tma_load_2d(dst, &tm_w, &full[s], (k_lo + kt) * 128, yw);
+          tma_load_2d(dst + LS_A_BYTES, &tm_x, &full[s], (k_lo + kt) * 128, yx);
+        }
       }
-      if (SVDQ_CHECK_OK((uint32_t)(dst - smem_raw) + stage_bytes <= dyn_smem_bytes(), 0x5c4))
-        tma_load_2d(dst + LS_A_BYTES, &tm_x, &full[s], (k_lo + kt) * 128, yx);
+      __syncwarp();
       issued = max(issued, kt + 1);
+      if (++s == a.stages) {
+        s = 0;
+        phase ^= 1u;
+      }
     }
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1) {
     const uint32_t idesc = idesc_i8(128, a.nt);
-    int kt = 0;
+    const uint64_t desc0 = sdesc_kmajor_sw128(smem_u32(smem));
+    int kt = 0, s = 0;
+    uint32_t phase = 0;
     for (; kt < nk; ++kt) {
-      const int s = kt % a.stages;
-      if (!mbar_wait_spin(&full[s], (uint32_t)((kt / a.stages) & 1), tmo, abort_flag, 0x532)) break;
+      if (!mbar_wait_warp(&full[s], phase, tmo, abort_flag, 0x532)) break;
       tc_fence_after();
-      const uint32_t base = smem_u32(smem + s * stage_bytes);
-      const uint64_t ad = sdesc_kmajor_sw128(base), bd = sdesc_kmajor_sw128(base + LS_A_BYTES);
+      const uint64_t ad = desc0 + (uint64_t)(s * (stage_bytes / 16)), bd = ad + LS_A_BYTES / 16;
+      if (elect_one()) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) tc_mma_i8(tbase, ad + 2 * j, bd + 2 * j, idesc, (kt | j) != 0 ? 1u : 0u);
-      if (kt + a.stages < nk) tc_commit(&empty[s]);      // nobody waits for the last round of slots
+        for (int j = 0; j < 4; ++j) tc_mma_i8(tbase, ad + 2 * j, bd + 2 * j, idesc, (kt | j) != 0 ? 1u : 0u);
+        if (kt + a.stages < nk) tc_commit(&empty[s]);    // nobody waits for the last round of slots
+        if (kt == nk - 1) tc_commit(acc_full);
+      }
+      __syncwarp();
+      if (++s == a.stages) {
+        s = 0;
+        phase ^= 1u;
+      }
     }
-    tc_commit(kt == nk ? acc_full : drain);
     if (kt < nk) {
       int never = 0;
+      if (elect_one()) tc_commit(drain);
+      __syncwarp();
       mbar_wait(drain, 0, tmo, &never, 0x534);
     }
   }
   __syncwarp();
 
   // ------------------------------------------------------------------ epilogue ---
-  if (warp != 0 || lane != 0) griddep_wait();            // the copying thread has waited
+  if (warp != 0) griddep_wait();                         // the copying warp has waited
   __syncwarp();
   griddep_launch_dependents();
+  const int tokens = min(a.nt, a.M - mb * a.nt);
+  const int n = nb * 128 + 4 * lane;                     // four channels a lane
+  float s4[4], b4[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    s4[i] = n + i < a.N ? __ldg(a.sw + n + i) : 0.0f;
+    b4[i] = a.bias && n + i < a.N ? __ldg(a.bias + n + i) : 0.0f;
+  }
+  for (int t = threadIdx.x; t < tokens; t += LS_THREADS) sxs[t] = __ldg(a.sx + mb * a.nt + t);
   const bool got = __all_sync(0xFFFFFFFFu, mbar_wait(acc_full, 0, tmo, abort_flag, 0x533));
   if (!got && warp == 0 && lane == 0) {                  // let the copies in flight land before the CTA exits
     int never = 0;
@@ -416,26 +485,20 @@ __global__ void __launch_bounds__(LS_THREADS) k_linear_i8_split(
     tc_fence_after();
     tmem_dealloc(tbase, cols);
   }
-  const int tokens = min(a.nt, a.M - mb * a.nt);
-  const int n = nb * 128 + 4 * lane;                     // four channels a lane
-  float s4[4], b4[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    s4[i] = n + i < a.N ? __ldg(a.sw + n + i) : 0.0f;
-    b4[i] = a.bias && n + i < a.N ? __ldg(a.bias + n + i) : 0.0f;
-  }
   const uint32_t mine = smem_u32(part) + 16u * (uint32_t)lane;
+#pragma unroll 4
   for (int t = rank + split * warp; t < tokens; t += split * (LS_THREADS / 32)) {
     int4 acc = make_int4(0, 0, 0, 0);
     for (int r = 0; r < split; ++r) {
-      const int4 v = ld_cluster_v4(split > 1 ? map_to_rank(mine + 512u * (uint32_t)t, (uint32_t)r) : mine + 512u * (uint32_t)t);
+      const int4 v = split > 1 ? ld_cluster_v4(map_to_rank(mine + 512u * (uint32_t)t, (uint32_t)r))
+                               : *reinterpret_cast<const int4*>(part + t * 128 + 4 * lane);
       acc.x += v.x;
       acc.y += v.y;
       acc.z += v.z;
       acc.w += v.w;
     }
     const int row = mb * a.nt + t;
-    const float sx = __ldg(a.sx + row);
+    const float sx = sxs[t];
     const float y0 = i8_dequant(acc.x, sx, s4[0], b4[0]), y1 = i8_dequant(acc.y, sx, s4[1], b4[1]);
     const float y2 = i8_dequant(acc.z, sx, s4[2], b4[2]), y3 = i8_dequant(acc.w, sx, s4[3], b4[3]);
     const int64_t at = (int64_t)row * a.ldy + n;

@@ -461,7 +461,7 @@ svdq_status check_shape_i8(int64_t M, int64_t N, int64_t K) {
 // Rows of `width` elements at pitch ld, at `p`: NULL, pitch and alignment (row_align: every row on 16 bytes).
 svdq_status check_rows(const void* p, int type, int64_t width, int64_t ld, bool row_align) {
   if (!p || ld < width) return SVDQ_ERR_INVALID_ARG;
-  if (ld > (int64_t(1) << 40)) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+  if (ld > (int64_t(1) << 37)) return SVDQ_ERR_UNSUPPORTED_SHAPE;
   if (!aligned16(p) || (row_align && ((uint64_t)ld * dtype_size(type)) % 16 != 0)) return SVDQ_ERR_MISALIGNED;
   return SVDQ_OK;
 }
@@ -499,11 +499,59 @@ int y_vector(const void* Y, int type, int64_t ldy) {
 
 std::atomic<bool> g_pair_attr[kMaxDevices], g_split_attr[kMaxDevices];
 
+// Which kernel, tile and K split serve a shape: the least of the times (microseconds) these lines predict,
+// fitted to a sweep of M 16..16384 by (N, K) of 320..12288 on a B200; a stage is 128 of K.
+//   pair kernel, nt channels a tile:   2.6 + main + (waves - 1) max(main, 1.65 + 0.0068 nt) + 0.3 + 0.0095 nt,
+//                                      main = stages (0.11 + 0.001 nt); later tiles hide their epilogue or wait for it
+//   split kernel, nt tokens, split s:  2.9 + 0.7 (s > 1: cluster reduction)
+//                                      + waves ((stages / s) (0.085 + 0.0015 nt) + nt (0.008 + 0.022 / s))
+// Splits of 5 and 7 are left out: clusters of that size leave SMs of a GPC idle.
+// (measured, both sides: 512 x 320 of K = 320: split nt 16 3.5 us, pair nt 64 4.1; 128 x 4096 of K = 4096: split
+// nt 64, s 2 7.9, pair nt 64 9.0; 256 x 4096 of K = 4096: pair nt 64 8.9, split nt 64, s 2 10.7.)
+struct LinearI8Plan {
+  bool pair;
+  int nt, split;
+};
+LinearI8Plan plan_linear_i8(int64_t M, int64_t N, int64_t K, int sms) {
+  const int64_t nkt = (K + 127) / 128;
+  LinearI8Plan best = {true, 256, 1};
+  double least = 1e30;
+  const auto waves = [](int64_t tiles, int64_t at_once) { return (double)((tiles + at_once - 1) / at_once); };
+  for (int nt = 256; nt >= 64; nt -= 64) {
+    const int64_t tiles = (M + 255) / 256 * ((N + nt - 1) / nt);
+    const double main = (double)nkt * (0.11 + 0.001 * nt);
+    const double t = 2.6 + main + (waves(tiles, sms / 2) - 1) * std::max(main, 1.65 + 0.0068 * nt) + 0.3 + 0.0095 * nt;
+    if (t < least) {
+      least = t;
+      best = {true, nt, 1};
+    }
+  }
+  const int m16 = (int)std::min<int64_t>((M + 15) / 16 * 16, 128);   // all the tokens, where they fit a tile
+  for (int nt = 16; nt <= 128; nt *= 2) {
+    const int tok = std::min(nt, m16);
+    const int64_t tiles = (M + tok - 1) / tok * ((N + 127) / 128);
+    if (tiles > 4 * (int64_t)sms || (M + tok - 1) / tok > 65535) continue;
+    for (const int s : {1, 2, 3, 4, 6, 8}) {
+      if (s > 1 && (tiles * s > sms || 2 * s > nkt)) break;
+      const double t = 2.9 + (s > 1 ? 0.7 : 0.0) +
+                       waves(tiles * s, sms) * ((double)((nkt + s - 1) / s) * (0.085 + 0.0015 * tok) +
+                                                tok * (0.008 + 0.022 / s));
+      if (t < least) {
+        least = t;
+        best = {false, tok, s};
+      }
+    }
+    if (nt >= m16) break;
+  }
+  return best;
+}
+
 // w_early: the kernel before this one on the stream is a quantizer of this library, which has waited for
 // everything before it, so the weight may be read while it still runs.
 svdq_status launch_linear_i8(int dev, DevInfo* d, const int8_t* Xq, const float* sx, const int8_t* Wq,
                              const float* sw, const float* bias, void* Y, int y_type, int64_t ldy, int64_t M,
                              int64_t N, int64_t K, int w_early, cudaStream_t s) {
+  const LinearI8Plan p = plan_linear_i8(M, N, K, d->sms);
   LinearI8Args a;
   a.sx = sx;
   a.sw = sw;
@@ -515,50 +563,33 @@ svdq_status launch_linear_i8(int dev, DevInfo* d, const int8_t* Xq, const float*
   a.M = (int)M;
   a.N = (int)N;
   a.K = (int)K;
+  a.nt = p.nt;
   a.w_early = w_early;
   a.stages = 0;
-  svdq_status st;
-  const int nkt = (int)((K + 127) / 128);
   CUtensorMap tm_x, tm_w;
-  if (M <= 256) {
-    a.nt = (int)((M + 15) / 16 * 16);
-    const int stage = LS_A_BYTES + a.nt * 128;
-    const int budget = a.nt <= 128 ? 100 * 1024 : 200 * 1024;
-    const int slots = d->sms * (a.nt <= 128 ? 2 : 1);
-    const int tiles = (int)((N + 127) / 128);
-    int split = 1;
-    while (split < 8 && (int64_t)tiles * (split + 1) <= slots && nkt >= 2 * (split + 1)) ++split;
-    const int per = (nkt + split - 1) / split;
-    a.stages = std::max(1, std::min(std::min(per, budget / stage), 12));
-    const size_t smem = (size_t)std::max(a.stages * stage, a.nt * 512) + LS_BAR_BYTES + 1024;
-    if (!make_map_2d(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, Wq, (uint64_t)K, (uint64_t)N, (uint64_t)K, 128, 128) ||
-        !make_map_2d(&tm_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, Xq, (uint64_t)K, (uint64_t)M, (uint64_t)K, 128,
-                     (uint32_t)a.nt))
-      return SVDQ_ERR_CUDA;
-    if ((st = allow_smem(k_linear_i8_split, dev, g_split_attr, 200 * 1024 + LS_BAR_BYTES + 1024)) != SVDQ_OK) return st;
-    if (launch_pdl(k_linear_i8_split, dim3((unsigned)(tiles * split)), dim3(LS_THREADS), smem, s, split, tm_w, tm_x, a,
-                   split) != cudaSuccess)
+  if (!make_map_2d(&tm_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, Xq, (uint64_t)K, (uint64_t)M, (uint64_t)K, 128,
+                   (uint32_t)(p.pair ? 128 : p.nt)) ||
+      !make_map_2d(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, Wq, (uint64_t)K, (uint64_t)N, (uint64_t)K, 128,
+                   (uint32_t)(p.pair ? p.nt / 2 : 128)))
+    return SVDQ_ERR_CUDA;
+  svdq_status st;
+  if (p.pair) {
+    const int64_t tiles = (M + 255) / 256 * ((N + p.nt - 1) / p.nt);
+    if (tiles > kMaxDim) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+    if ((st = allow_smem(k_linear_i8_pair, dev, g_pair_attr, LP_SMEM)) != SVDQ_OK) return st;
+    if (launch_pdl(k_linear_i8_pair, dim3((unsigned)(2 * std::min<int64_t>(tiles, d->sms / 2))), dim3(LP_THREADS),
+                   (size_t)LP_SMEM, s, 2, tm_x, tm_w, a) != cudaSuccess)
       return SVDQ_ERR_CUDA;
     return launch_status();
   }
-  const int64_t num_m = (M + 255) / 256, pairs = d->sms / 2;
-  int64_t best = 0;
-  for (int nt = 256; nt >= 64; nt -= 64) {       // waves of tiles, a tile costing its columns and a fixed part
-    const int64_t cost = (num_m * ((N + nt - 1) / nt) + pairs - 1) / pairs * (nt + 24);
-    if (nt == 256 || cost < best) {
-      best = cost;
-      a.nt = nt;
-    }
-  }
-  if (!make_map_2d(&tm_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, Xq, (uint64_t)K, (uint64_t)M, (uint64_t)K, 128, 128) ||
-      !make_map_2d(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, Wq, (uint64_t)K, (uint64_t)N, (uint64_t)K, 128,
-                   (uint32_t)(a.nt / 2)))
-    return SVDQ_ERR_CUDA;
-  if ((st = allow_smem(k_linear_i8_pair, dev, g_pair_attr, LP_SMEM)) != SVDQ_OK) return st;
-  const int64_t tiles = num_m * ((N + a.nt - 1) / a.nt);
-  if (tiles > kMaxDim) return SVDQ_ERR_UNSUPPORTED_SHAPE;
-  if (launch_pdl(k_linear_i8_pair, dim3((unsigned)(2 * std::min(tiles, pairs))), dim3(LP_THREADS), (size_t)LP_SMEM, s, 2,
-                 tm_x, tm_w, a) != cudaSuccess)
+  // A ring of at most 100 KB: two CTAs fit an SM, so that the next kernel's start overlaps this one's end.
+  const int stage = LS_A_BYTES + p.nt * 128;
+  const int per = (int)(((K + 127) / 128 + p.split - 1) / p.split);
+  a.stages = std::min(per, 100 * 1024 / stage);
+  const size_t smem = (size_t)std::max(a.stages * stage, p.nt * 512) + LS_TAIL_BYTES + 1024;
+  if ((st = allow_smem(k_linear_i8_split, dev, g_split_attr, 100 * 1024 + LS_TAIL_BYTES + 1024)) != SVDQ_OK) return st;
+  if (launch_pdl(k_linear_i8_split, dim3((unsigned)((N + 127) / 128 * p.split), (unsigned)((M + p.nt - 1) / p.nt)),
+                 dim3(LS_THREADS), smem, s, p.split, tm_w, tm_x, a, p.split) != cudaSuccess)
     return SVDQ_ERR_CUDA;
   return launch_status();
 }

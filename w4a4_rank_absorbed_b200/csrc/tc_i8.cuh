@@ -48,6 +48,36 @@ SVDQ_DEV void tc_commit_pair(uint64_t* bar) {
                ::"r"(smem_u32(bar)), "h"((uint16_t)3) : "memory");
 }
 
+// ------------------------------------------------------- warp-uniform issuing ---
+// Copies and MMAs take their operands from uniform registers.  Where the compiler can prove a role's
+// control flow and operands uniform over the warp, an issue takes a few cycles; under a branch on the lane
+// it wraps each one in a loop over the active lanes (measured: 70 cycles an MMA, 600 a ring stage).  So a
+// role's whole warp walks its loop, values that come from shared memory or special registers pass through
+// warp_uniform, and only the issue itself is under elect_one().
+SVDQ_DEV uint32_t warp_uniform(uint32_t v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
+SVDQ_DEV bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+// mbar_wait_spin by a whole warp, with one answer for all its lanes.
+SVDQ_DEV bool mbar_wait_warp(uint64_t* bar, uint32_t parity, uint64_t timeout_ns, volatile int* abort, unsigned site) {
+  const uint32_t a = smem_u32(bar);
+  if (__all_sync(0xFFFFFFFFu, mbar_test_wait(a, parity))) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t n = 0;; ++n) {
+    if (__all_sync(0xFFFFFFFFu, mbar_test_wait(a, parity))) return true;
+    if ((n & 15u) == 15u && __any_sync(0xFFFFFFFFu, *abort != 0 || globaltimer_ns() - t0 > timeout_ns)) {
+      if (elect_one() && !*abort) {
+        *abort = 1;
+        report_timeout(site);
+      }
+      __syncwarp();
+      return false;
+    }
+  }
+}
+
 // ---------------------------------------------------------------- clusters ---
 SVDQ_DEV uint32_t cluster_rank() {
   uint32_t r;
