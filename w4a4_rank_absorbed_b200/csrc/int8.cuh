@@ -17,7 +17,7 @@ namespace svdq {
 
 enum : int { DT_BF16 = 0, DT_FP32 = 1, DT_FP16 = 2 };
 
-// 16 consecutive bytes of a row hold Elem<T>::kVec elements; a vector of 8 elements is kRegs words.
+// Element types: 8 consecutive elements are kWords 32-bit words.
 template <typename T>
 struct Elem;
 template <>
@@ -146,44 +146,152 @@ __global__ void __launch_bounds__(PW8_THREADS) k_pack_weight_i8(const float* __r
   }
 }
 
-// Activation quantization: one block per row, two passes over it (the second from cache).
+// Eight codes of x_hat = x s as one byte each: f32(x_hat mul) plus 1.5 2^23 leaves rint of it (to even, as the
+// sum is rounded to whole numbers) in the low bits of the sum, whose low byte is the code.
+SVDQ_DEV uint2 i8_codes(const float (&x)[8], const float (&s)[8], float mul) {
+  uint32_t c[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 xh = mul_f32x2(make_float2(x[2 * i], x[2 * i + 1]), make_float2(s[2 * i], s[2 * i + 1]));
+    // (not as packed pairs: a packed product and sum came out as one fused operation, off at ties)
+    c[2 * i] = __float_as_uint(__fadd_rn(__fmul_rn(xh.x, mul), 12582912.0f));
+    c[2 * i + 1] = __float_as_uint(__fadd_rn(__fmul_rn(xh.y, mul), 12582912.0f));
+  }
+  return make_uint2(__byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410),
+                    __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410));
+}
+
+// Activation quantization.  A group of threads, a warp or a block, owns a row at a time, each thread VPT vectors
+// of 8 elements of it (vector j at its index + j times the group's size), the same columns in every row, so
+// that their smoothing factors stay in registers; X is read once and held in registers between the maximum
+// and the codes, and the group's next row is on its way while this one is reduced.
+// HBM-bound for many rows (3 K bytes a 16-bit row).  Measured: 18432 x 4096 40.6 us, 0.86 of the copy
+// bandwidth; 4608 x 4096 12.1 us, 0.72 (18.1 with four rows and 512 threads a block, whose registers left one
+// block an SM); one row of 4096 1.6 us.  Up to 1024 columns a warp holds a row, without barriers (16384 x
+// 320: 5.3 us, 5.8 with a block a row), unless the rows are too few to fill the GPU with warps (77 x 640: 1.9 us,
+// 1.5 with a block); up to 16384 a block does; beyond that k_quantize_long_i8 reads rows twice.
+constexpr int QI_MAX_THREADS = 512;
+template <typename T, int VPT, bool WARP>
+__global__ void __launch_bounds__(WARP ? 256 : QI_MAX_THREADS) k_quantize_act_i8(
+    const T* __restrict__ X, int64_t M, int K, int64_t ldx, const float* __restrict__ inv_s, int8_t* __restrict__ Xq,
+    float* __restrict__ sx) {
+  constexpr int W = Elem<T>::kWords;
+  __shared__ uint32_t part[2][QI_MAX_THREADS / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int me = WARP ? lane : threadIdx.x, size = WARP ? 32 : blockDim.x;
+  const int64_t step = WARP ? (int64_t)gridDim.x * (blockDim.x >> 5) : gridDim.x;
+  const int nv = K >> 3;
+  // Everything earlier on the stream is done before this grid lets its dependent start (k_linear_i8_split's
+  // early weight copies rest on that).
+  griddep_wait();
+  griddep_launch_dependents();
+  float s[VPT][8];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int v = me + j * size;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[j][i] = 1.0f;
+    if (inv_s && v < nv) {
+      const float4 s0 = __ldg(reinterpret_cast<const float4*>(inv_s) + 2 * v);
+      const float4 s1 = __ldg(reinterpret_cast<const float4*>(inv_s) + 2 * v + 1);
+      s[j][0] = s0.x; s[j][1] = s0.y; s[j][2] = s0.z; s[j][3] = s0.w;
+      s[j][4] = s1.x; s[j][5] = s1.y; s[j][6] = s1.z; s[j][7] = s1.w;
+    }
+  }
+  uint32_t w[VPT][W], nx[VPT][W];
+  const auto fetch = [&](int64_t row, uint32_t(&d)[VPT][W]) {
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int v = me + j * size;
+      if (v < nv && row < M) {
+        load8(X + row * ldx + 8 * v, d[j]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i) d[j][i] = 0u;
+      }
+    }
+  };
+  int buf = 0;
+  int64_t row = WARP ? (int64_t)blockIdx.x * (blockDim.x >> 5) + warp : blockIdx.x;
+  fetch(row, w);
+  for (; row < M; row += step) {                         // uniform over the group
+    fetch(row + step, nx);
+    uint32_t a = 0u;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      float f[8];
+      Elem<T>::unpack(w[j], f);
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        const float2 h = mul_f32x2(make_float2(f[i], f[i + 1]), make_float2(s[j][i], s[j][i + 1]));
+        a = umax(a, umax(abs_bits(h.x), abs_bits(h.y)));
+      }
+    }
+    a = __reduce_max_sync(0xFFFFFFFFu, a);
+    if (!WARP) {
+      if (lane == 0) part[buf][warp] = a;                // two buffers: one barrier a row
+      __syncthreads();
+      a = __reduce_max_sync(0xFFFFFFFFu, lane < (size >> 5) ? part[buf][lane] : 0u);
+      buf ^= 1;
+    }
+    float scale, mul;
+    i8_scale(a, scale, mul);
+    if (me == 0) sx[row] = scale;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int v = me + j * size;
+      if (v < nv) {
+        float f[8];
+        Elem<T>::unpack(w[j], f);
+        const uint2 c = i8_codes(f, s[j], mul);
+        // where the multiplier is 0 the row has no codes (0 times an infinite element has none)
+        *reinterpret_cast<uint2*>(Xq + row * K + 8 * v) = mul == 0.0f ? make_uint2(0u, 0u) : c;
+      }
+#pragma unroll
+      for (int i = 0; i < W; ++i) w[j][i] = nx[j][i];
+    }
+  }
+}
+
+// Rows of more than 16384 columns: a block per row, read once for the maximum and again (from cache) for the codes.
 template <typename T>
-__global__ void __launch_bounds__(256) k_quantize_act_i8(const T* __restrict__ X, int K, int64_t ldx,
-                                                         const float* __restrict__ inv_s, int8_t* __restrict__ Xq,
-                                                         float* __restrict__ sx) {
-  __shared__ uint32_t part[8];
+__global__ void __launch_bounds__(QI_MAX_THREADS) k_quantize_long_i8(const T* __restrict__ X, int K, int64_t ldx,
+                                                                     const float* __restrict__ inv_s,
+                                                                     int8_t* __restrict__ Xq, float* __restrict__ sx) {
+  __shared__ uint32_t part[QI_MAX_THREADS / 32];
   griddep_wait();
   griddep_launch_dependents();
   const int64_t m = blockIdx.x;
   const T* row = X + m * ldx;
-  const int nv = K >> 3;
-  uint32_t a = 0u;
-  for (int v = threadIdx.x; v < nv; v += 256) {
+  const int nv = K >> 3, lane = threadIdx.x & 31;
+  const auto fetch = [&](int v, float(&f)[8], float(&s)[8]) {
     uint32_t w[Elem<T>::kWords];
-    float f[8];
     load8(row + 8 * v, w);
     Elem<T>::unpack(w, f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a = umax(a, abs_bits(inv_s ? __fmul_rn(f[i], __ldg(inv_s + 8 * v + i)) : f[i]));
+    for (int i = 0; i < 8; ++i) s[i] = inv_s ? __ldg(inv_s + 8 * v + i) : 1.0f;
+  };
+  uint32_t a = 0u;
+#pragma unroll 4
+  for (int v = threadIdx.x; v < nv; v += QI_MAX_THREADS) {
+    float f[8], s[8];
+    fetch(v, f, s);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a = umax(a, abs_bits(__fmul_rn(f[i], s[i])));
   }
   a = __reduce_max_sync(0xFFFFFFFFu, a);
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = a;
+  if (lane == 0) part[threadIdx.x >> 5] = a;
   __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 8; ++i) a = umax(a, part[i]);
+  a = __reduce_max_sync(0xFFFFFFFFu, part[lane & (QI_MAX_THREADS / 32 - 1)]);
   float scale, mul;
   i8_scale(a, scale, mul);
   if (threadIdx.x == 0) sx[m] = scale;
-  for (int v = threadIdx.x; v < nv; v += 256) {
-    uint32_t w[Elem<T>::kWords];
-    float f[8];
-    int q[8];
-    load8(row + 8 * v, w);
-    Elem<T>::unpack(w, f);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = i8_code(inv_s ? __fmul_rn(f[i], __ldg(inv_s + 8 * v + i)) : f[i], mul);
-    *reinterpret_cast<uint2*>(Xq + m * K + 8 * v) =
-        make_uint2(pack_i8x4(q[0], q[1], q[2], q[3]), pack_i8x4(q[4], q[5], q[6], q[7]));
+#pragma unroll 4
+  for (int v = threadIdx.x; v < nv; v += QI_MAX_THREADS) {
+    float f[8], s[8];
+    fetch(v, f, s);
+    const uint2 c = i8_codes(f, s, mul);
+    *reinterpret_cast<uint2*>(Xq + m * K + 8 * v) = mul == 0.0f ? make_uint2(0u, 0u) : c;
   }
 }
 

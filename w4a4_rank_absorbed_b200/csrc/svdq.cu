@@ -466,19 +466,45 @@ svdq_status check_rows(const void* p, int type, int64_t width, int64_t ld, bool 
   return SVDQ_OK;
 }
 
-svdq_status launch_quantize_i8(const void* X, int x_type, int64_t ldx, int64_t M, int64_t K, const float* inv_s,
-                               int8_t* Xq, float* sx, cudaStream_t s) {
-  cudaError_t e;
-  if (x_type == SVDQ_BF16)
-    e = launch_pdl(k_quantize_act_i8<__nv_bfloat16>, dim3((unsigned)M), dim3(256), 0, s, 1,
-                   static_cast<const __nv_bfloat16*>(X), (int)K, ldx, inv_s, Xq, sx);
-  else if (x_type == SVDQ_FP16)
-    e = launch_pdl(k_quantize_act_i8<__half>, dim3((unsigned)M), dim3(256), 0, s, 1, static_cast<const __half*>(X),
-                   (int)K, ldx, inv_s, Xq, sx);
-  else
-    e = launch_pdl(k_quantize_act_i8<float>, dim3((unsigned)M), dim3(256), 0, s, 1, static_cast<const float*>(X),
-                   (int)K, ldx, inv_s, Xq, sx);
+template <typename T, int VPT, bool WARP>
+cudaError_t run_quantize_i8(DevInfo* d, const T* X, int64_t M, int64_t K, int64_t ldx, const float* inv_s, int8_t* Xq,
+                            float* sx, cudaStream_t s) {
+  const int threads = WARP ? 256 : (int)((K / 8 + VPT - 1) / VPT + 31) / 32 * 32;
+  const int rows = WARP ? 8 : 1;                                     // rows a block takes at a time
+  // As many blocks as are at work at one time: each then fetches rows ahead of the ones it reduces.
+  static std::atomic<int> resident[QI_MAX_THREADS / 32 + 1];         // per SM, by warps of a block; 0: not asked yet
+  int per_sm = resident[threads / 32].load(std::memory_order_relaxed);
+  if (per_sm == 0) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k_quantize_act_i8<T, VPT, WARP>, threads, 0) !=
+        cudaSuccess)
+      return cudaErrorUnknown;
+    resident[threads / 32].store(per_sm = std::max(1, per_sm), std::memory_order_relaxed);
+  }
+  const int64_t blocks = std::min<int64_t>((M + rows - 1) / rows, (int64_t)d->sms * per_sm);
+  return launch_pdl(k_quantize_act_i8<T, VPT, WARP>, dim3((unsigned)blocks), dim3(threads), 0, s, 1, X, M, (int)K, ldx,
+                    inv_s, Xq, sx);
+}
+template <typename T>
+svdq_status quantize_i8(DevInfo* d, const void* Xv, int64_t ldx, int64_t M, int64_t K, const float* inv_s, int8_t* Xq,
+                        float* sx, cudaStream_t s) {
+  const T* X = static_cast<const T*>(Xv);
+  const int64_t nv = K / 8;                                          // vectors of 8 in a row
+  const bool warps = M > 4 * (int64_t)d->sms;                        // enough rows for a warp each
+  const cudaError_t e =
+      warps && nv <= 32    ? run_quantize_i8<T, 1, true>(d, X, M, K, ldx, inv_s, Xq, sx, s)
+      : warps && nv <= 64  ? run_quantize_i8<T, 2, true>(d, X, M, K, ldx, inv_s, Xq, sx, s)
+      : warps && nv <= 128 ? run_quantize_i8<T, 4, true>(d, X, M, K, ldx, inv_s, Xq, sx, s)
+      : nv <= 1024         ? run_quantize_i8<T, 2, false>(d, X, M, K, ldx, inv_s, Xq, sx, s)
+      : nv <= 2048         ? run_quantize_i8<T, 4, false>(d, X, M, K, ldx, inv_s, Xq, sx, s)
+                           : launch_pdl(k_quantize_long_i8<T>, dim3((unsigned)M), dim3(QI_MAX_THREADS), 0, s, 1, X,
+                                        (int)K, ldx, inv_s, Xq, sx);
   return e == cudaSuccess ? launch_status() : SVDQ_ERR_CUDA;
+}
+svdq_status launch_quantize_i8(DevInfo* d, const void* X, int x_type, int64_t ldx, int64_t M, int64_t K,
+                               const float* inv_s, int8_t* Xq, float* sx, cudaStream_t s) {
+  if (x_type == SVDQ_BF16) return quantize_i8<__nv_bfloat16>(d, X, ldx, M, K, inv_s, Xq, sx, s);
+  if (x_type == SVDQ_FP16) return quantize_i8<__half>(d, X, ldx, M, K, inv_s, Xq, sx, s);
+  return quantize_i8<float>(d, X, ldx, M, K, inv_s, Xq, sx, s);
 }
 
 // Shared memory a kernel may use, raised once per device and kernel.
@@ -835,7 +861,7 @@ svdq_status svdq_quantize_act_i8(const void* X, int x_type, int64_t ldx, int64_t
   int dev;
   DevInfo* d;
   if ((st = current_device(&dev, &d)) != SVDQ_OK) return st;
-  return launch_quantize_i8(X, x_type, ldx, M, K, inv_s, Xq, sx, reinterpret_cast<cudaStream_t>(stream));
+  return launch_quantize_i8(d, X, x_type, ldx, M, K, inv_s, Xq, sx, reinterpret_cast<cudaStream_t>(stream));
 }
 
 svdq_status svdq_linear_i8(const int8_t* Xq, const float* sx, const int8_t* Wq, const float* sw, const float* bias,
@@ -879,7 +905,7 @@ svdq_status svdq_forward_i8(const void* X, int x_type, int64_t ldx, const float*
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int8_t* Xq = static_cast<int8_t*>(workspace);           // M x K codes (K % 16 == 0), then the M scales
   float* sx = reinterpret_cast<float*>(Xq + (size_t)M * (size_t)K);
-  if ((st = launch_quantize_i8(X, x_type, ldx, M, K, inv_s, Xq, sx, s)) != SVDQ_OK) return st;
+  if ((st = launch_quantize_i8(d, X, x_type, ldx, M, K, inv_s, Xq, sx, s)) != SVDQ_OK) return st;
   return launch_linear_i8(dev, d, Xq, sx, Wq, sw, bias, Y, y_type, ldy, M, N, K, 1, s);
 }
 
