@@ -621,9 +621,33 @@ svdq_status launch_linear_i8(int dev, DevInfo* d, const int8_t* Xq, const float*
 }
 
 // ------------------------------------------------------------- group norm ---
-constexpr int64_t kMaxNormC = 4096;
+constexpr int64_t kMaxNormC = GN_MAX_C;
 
-size_t group_norm_workspace(int64_t B, int64_t G) { return (size_t)B * (size_t)G * sizeof(float2); }
+constexpr int64_t kNormBlocks = 148;      // blocks at work at one time: one an SM of a B200
+constexpr int64_t kNormMerge = 8192;      // partial entries a sample above which a launch of its own merges them
+
+struct NormPlan {
+  int nv, rp, threads, P, rows;
+  bool merge;
+};
+// Rows are dealt to as many blocks as the GPU holds at one time, over all samples, as long as each thread keeps
+// about four rows (fewer leave a block nothing to have in flight).
+NormPlan plan_norm(int64_t B, int64_t S, int64_t C, int64_t G) {
+  NormPlan p;
+  p.nv = (int)((C + 7) / 8);
+  p.rp = (int)std::min<int64_t>(std::max(1, GN_MAX_THREADS / p.nv), S);
+  p.threads = (p.nv * p.rp + 31) / 32 * 32;
+  p.P = (int)std::max<int64_t>(1, std::min<int64_t>(kNormBlocks / B, S / (p.rp * 4)));
+  p.rows = (int)((S + p.P - 1) / p.P);
+  p.P = (int)((S + p.rows - 1) / p.rows);
+  p.merge = (int64_t)p.P * G > kNormMerge;
+  return p;
+}
+
+size_t group_norm_workspace(int64_t B, int64_t S, int64_t C, int64_t G) {
+  const NormPlan p = plan_norm(B, S, C, G);
+  return (size_t)B * (size_t)G * (size_t)(p.P + (p.merge ? 1 : 0)) * sizeof(float2);
+}
 
 struct NormArgs {
   const void* X;
@@ -641,17 +665,53 @@ struct NormArgs {
   size_t ws_bytes;
 };
 
-template <typename T, bool QUANT>
+template <typename T, bool VEC, bool QUANT>
 svdq_status launch_norm(const NormArgs& n, cudaStream_t s) {
-  const T* X = static_cast<const T*>(n.X);
-  float2* stats = static_cast<float2*>(n.ws);
-  if (launch_pdl(k_group_stats<T>, dim3((unsigned)(n.B * n.G)), dim3(256), 0, s, 1, X, n.S, (int)n.C, n.ldx, (int)n.G,
-                 n.eps, stats) != cudaSuccess ||
-      launch_pdl(k_group_apply<T, QUANT>, dim3((unsigned)(n.B * n.S)), dim3(256), 0, s, 1, X, n.S, (int)n.C, n.ldx,
-                 (int)n.G, (const float2*)stats, n.gamma, n.beta, n.act, static_cast<T*>(n.Y), n.ldy, n.inv_s, n.Xq,
-                 n.sx) != cudaSuccess)
+  const NormPlan p = plan_norm(n.B, n.S, n.C, n.G);
+  GroupNormArgs a;
+  a.X = n.X;
+  a.ldx = n.ldx;
+  a.S = (int)n.S;
+  a.C = (int)n.C;
+  a.G = (int)n.G;
+  a.nv = p.nv;
+  a.rp = p.rp;
+  a.P = p.P;
+  a.rows = a.part_rows = p.rows;
+  a.parts = p.P;
+  a.part = static_cast<float2*>(n.ws);
+  a.gamma = n.gamma;
+  a.beta = n.beta;
+  a.eps = n.eps;
+  a.act = n.act;
+  a.streaming = (int64_t)n.B * n.S * n.C * (int64_t)sizeof(T) > (int64_t(48) << 20);
+  a.Y = n.Y;
+  a.ldy = n.ldy;
+  a.inv_s = n.inv_s;
+  a.Xq = n.Xq;
+  a.sx = n.sx;
+  const int64_t blocks = n.B * p.P;
+  if (launch_pdl(k_group_stats<T, VEC>, dim3((unsigned)blocks), dim3(p.threads), 0, s, 1, a) != cudaSuccess)
+    return SVDQ_ERR_CUDA;
+  if (p.merge) {
+    const int64_t bg = n.B * n.G;
+    float2* merged = a.part + bg * p.P;
+    if (launch_pdl(k_group_merge, dim3((unsigned)((bg + 7) / 8)), dim3(256), 0, s, 1, (const float2*)a.part, bg, a.G, p.P,
+                   p.rows, a.S, a.C / a.G, merged) != cudaSuccess)
+      return SVDQ_ERR_CUDA;
+    a.part = merged;
+    a.parts = 1;
+    a.part_rows = a.S;
+  }
+  const size_t smem = (size_t)n.G * sizeof(float2) + (QUANT ? 3 * GN_QROWS * p.rp * sizeof(uint32_t) : 0);
+  if (launch_pdl(k_group_apply<T, VEC, QUANT>, dim3((unsigned)blocks), dim3(p.threads), smem, s, 1, a) != cudaSuccess)
     return SVDQ_ERR_CUDA;
   return launch_status();
+}
+template <typename T, bool QUANT>
+svdq_status launch_norm(const NormArgs& n, cudaStream_t s) {
+  const bool vec = n.C % 8 == 0 && n.ldx * sizeof(T) % 16 == 0 && (QUANT || n.ldy * sizeof(T) % 16 == 0);
+  return vec ? launch_norm<T, true, QUANT>(n, s) : launch_norm<T, false, QUANT>(n, s);
 }
 
 template <bool QUANT>
@@ -671,7 +731,7 @@ svdq_status norm_impl(const NormArgs& n, cudaStream_t s) {
   } else if ((st = check_rows(n.Y, n.type, n.C, n.ldy, false)) != SVDQ_OK) {
     return st;
   }
-  if (!n.ws || n.ws_bytes < group_norm_workspace(n.B, n.G)) return SVDQ_ERR_INVALID_ARG;
+  if (!n.ws || n.ws_bytes < group_norm_workspace(n.B, n.S, n.C, n.G)) return SVDQ_ERR_INVALID_ARG;
   if (!aligned16(n.ws) || (n.gamma && !aligned16(n.gamma)) || (n.beta && !aligned16(n.beta))) return SVDQ_ERR_MISALIGNED;
   int dev;
   DevInfo* d;
@@ -910,8 +970,9 @@ svdq_status svdq_forward_i8(const void* X, int x_type, int64_t ldx, const float*
 }
 
 size_t svdq_group_norm_workspace_bytes(int64_t B, int64_t S, int64_t C, int64_t G) {
-  if (B < 1 || S < 1 || C < 1 || G < 1 || C % G != 0 || C > kMaxNormC || B > kMaxDim) return 0;
-  return group_norm_workspace(B, G);
+  if (B < 1 || S < 1 || C < 1 || G < 1 || C % G != 0 || C > kMaxNormC || B > kMaxDim || S > kMaxDim / B)
+    return 0;
+  return group_norm_workspace(B, S, C, G);
 }
 
 svdq_status svdq_group_norm(const void* X, int type, int64_t ldx, int64_t B, int64_t S, int64_t C, int64_t G,
