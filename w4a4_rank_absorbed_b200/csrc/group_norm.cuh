@@ -3,20 +3,24 @@
 //   sample and the C / G channels of a group
 //
 // Bound by memory: x read, y written, 4 bytes an element for 16-bit types.  Every output needs every input of
-// its group, so x is read twice, the second time from L2 as far as it holds it: two launches over the same
-// rows, the second a programmatic dependent of the first and walking its rows backwards (the rows read last
-// are the ones L2 still has).  Between them each block of the first leaves (mean, M2) of its rows per group,
-// and each block of the second merges those of its sample: nothing needs clearing beforehand, no block
-// waits for another, and the order of every sum is fixed.
+// its group, so there are two passes over the rows, in one of two forms:
+//   k_group_norm   one launch; the blocks of a sample (up to eight, a cluster) keep its rows in shared memory between
+//                  the passes and merge their statistics there: x is read once.  For samples that fit.
+//   k_group_stats, k_group_apply   two launches over the same blocks of rows, the second a programmatic dependent of
+//                  the first and walking its rows backwards (the rows read last are the ones L2 still has).
+//                  Each block of the first leaves (mean, M2) of its rows per group, each block of the second
+//                  merges those of its sample: nothing needs clearing, no block waits for another.
+// The order of every sum is fixed.
 //
 // Statistics: a thread owns 8 consecutive channels (a 16-byte vector of a 16-bit type) of every rp-th row,
-// whichever groups they fall in, and sums x - p and its square per channel, p the block's first row: p lies in
-// the channel's own range, so the squares do not cancel however far the mean is from zero.  Channels, blocks and
-// groups are then merged by n, mean and M2 = sum (x - mean)^2 (T. F. Chan, G. H. Golub and R. J. LeVeque, "Updating
+// whichever groups they fall in, and sums x - p and its square per channel, p the first channel of the group in the
+// block's first row: p lies in the group's own range, so the squares do not cancel however far the mean is from
+// zero.  Blocks are merged by n, mean and M2 = sum (x - mean)^2 (T. F. Chan, G. H. Golub and R. J. LeVeque, "Updating
 // formulae and a pairwise algorithm for computing sample variances", 1979).
 #pragma once
 #include "gelu.cuh"
 #include "int8.cuh"
+#include "tc_i8.cuh"
 
 namespace svdq {
 
@@ -24,22 +28,20 @@ enum : int { ACT_NONE = 0, ACT_SILU = 1, ACT_GELU = 2 };
 
 constexpr int GN_MAX_THREADS = 512;
 constexpr int GN_MAX_C = 8 * GN_MAX_THREADS;
-// Rows a thread has in flight: 128 bytes of them.
+// Rows a thread has in flight, 64 bytes of them.
 template <typename T>
-constexpr int GN_UNROLL = 16 / (int)sizeof(T);
-constexpr int GN_QROWS = 4;                    // rows a thread quantizes at a time
+constexpr int GN_UNROLL = 8 / (int)sizeof(T);
 
 struct GroupNormArgs {
   const void* X;
   int64_t ldx;
   int S, C, G;
   int nv;                 // 8-channel vectors a row, the last one possibly short
-  int rp;                 // rows a block takes at a time: threads / nv
+  int rp1;                // first pass: nv threads a row, rp1 rows at a time
+  int l2, rp2;            // second pass: l2 threads a row (nv, or for codes whole warps or a power of two), rp2 rows
   int P;                  // blocks a sample, of `rows` rows each, the last one what is left
   int rows;
-  int parts;              // entries of part a sample: the first pass's blocks, or 1 once merged (of part_rows rows)
-  int part_rows;
-  float2* part;           // [sample][parts][G]: (mean, M2) of a block's rows
+  float2* part;           // [sample][P][G]: (mean, M2) of a block's rows
   const float* gamma;
   const float* beta;
   float eps;
@@ -93,42 +95,59 @@ SVDQ_DEV void gn_load(const T* p, int c, int C, uint32_t (&w)[Elem<T>::kWords]) 
 
 // M2 is never negative but for rounding; a NaN stays one.
 SVDQ_DEV float gn_m2(float v) { return v < 0.0f ? 0.0f : v; }
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(GN_MAX_THREADS) k_group_stats(const GroupNormArgs a) {
+
+// First pass over the block's rows lo..hi: (mean, M2) of each group to out (shared or global memory).  sum and
+// sq: 8 floats a thread each.  KEEP: the rows also go to `kept` (row by row, nv vectors).
+template <typename T, bool VEC, bool KEEP>
+SVDQ_DEV void gn_block_stats(const GroupNormArgs& a, const T* X, int lo, int hi, float* sum, float* sq, uint4* kept,
+                             float2* out) {
   constexpr int W = Elem<T>::kWords, U = GN_UNROLL<T>;
-  __shared__ float sum[GN_MAX_C], sq[GN_MAX_C];          // [row slot][8 nv]: at most 8 values a thread
-  const int b = blockIdx.x / a.P, p = blockIdx.x % a.P;
-  const int lo = p * a.rows, hi = min(a.S, lo + a.rows);
-  const int slot = threadIdx.x / a.nv, v = threadIdx.x % a.nv, c = 8 * v;
-  const int width = 8 * a.nv;
-  const T* X = static_cast<const T*>(a.X) + (int64_t)b * a.S * a.ldx;
-  griddep_wait();
-  griddep_launch_dependents();
-  float pivot[8], s[8], q[8];
-  if (slot < a.rp) {
-    uint32_t w[W];
-    gn_load<T, VEC>(X + lo * a.ldx, c, a.C, w);
-    Elem<T>::unpack(w, pivot);
+  const int slot = threadIdx.x / a.nv, v = threadIdx.x - slot * a.nv, c = 8 * v;
+  const int width = 8 * a.nv, cg = a.C / a.G, lane = threadIdx.x & 31;
+  if (slot < a.rp1) {
+    uint32_t x[U][W], nx[U][W];
+    const auto fetch = [&](int r0, uint32_t(&x)[U][W]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s[i] = q[i] = 0.0f;
-    const auto add = [&](const uint32_t(&d)[W]) {
-      float f[8];
-      Elem<T>::unpack(d, f);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float e = f[i] - pivot[i];
-        s[i] += e;
-        q[i] = fmaf(e, e, q[i]);
-      }
+      for (int u = 0; u < U; ++u)
+        if (r0 + u * a.rp1 < hi) gn_load<T, VEC>(X + (int64_t)(r0 + u * a.rp1) * a.ldx, c, a.C, x[u]);
     };
-    for (int r0 = lo + slot; r0 < hi; r0 += U * a.rp) {
-      uint32_t x[U][W];
+    fetch(lo + slot, x);                                 // in flight together with the pivots
+    float pivot[8], s[8], q[8];
+    int first = c / cg * cg, left = first + cg - c;      // the vector's channels, group by group
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (left == 0 && c + i < a.C) {
+        first += cg;
+        left = cg;
+      }
+      --left;
+      pivot[i] = Elem<T>::to_f32(X[(int64_t)lo * a.ldx + first]);
+      s[i] = q[i] = 0.0f;
+    }
+    for (int r0 = lo + slot; r0 < hi; r0 += U * a.rp1) {
+      fetch(r0 + U * a.rp1, nx);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int r = r0 + u * a.rp1;
+        if (r >= hi) continue;
+        float f[8];
+        Elem<T>::unpack(x[u], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float e = f[i] - pivot[i];
+          s[i] += e;
+          q[i] = fmaf(e, e, q[i]);
+        }
+        if (KEEP) {
+          uint4* k = kept + ((r - lo) * a.nv + v) * (W / 4);
+#pragma unroll
+          for (int i = 0; i < W / 4; ++i) k[i] = make_uint4(x[u][4 * i], x[u][4 * i + 1], x[u][4 * i + 2], x[u][4 * i + 3]);
+        }
+      }
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (r0 + u * a.rp < hi) gn_load<T, VEC>(X + (int64_t)(r0 + u * a.rp) * a.ldx, c, a.C, x[u]);
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (r0 + u * a.rp < hi) add(x[u]);
+        for (int i = 0; i < W; ++i) x[u][i] = nx[u][i];
     }
 #pragma unroll
     for (int i = 0; i < 8; i += 4) {
@@ -136,8 +155,8 @@ __global__ void __launch_bounds__(GN_MAX_THREADS) k_group_stats(const GroupNormA
       *reinterpret_cast<float4*>(sq + slot * width + c + i) = make_float4(q[i], q[i + 1], q[i + 2], q[i + 3]);
     }
   }
-  // the row slots' sums: folded in half while there are many, then one channel a thread
-  int n = a.rp;
+  // row slots folded in half while there are many
+  int n = a.rp1;
   for (; n > 8;) {
     const int h = (n + 1) >> 1;
     __syncthreads();
@@ -148,122 +167,138 @@ __global__ void __launch_bounds__(GN_MAX_THREADS) k_group_stats(const GroupNormA
     n = h;
   }
   __syncthreads();
-  // mean (less the pivot) and M2 of each channel, in place
-  const float rows = (float)(hi - lo), inv = 1.0f / rows;
-  for (int i = threadIdx.x; i < width; i += blockDim.x) {
-    float s1 = sum[i], q1 = sq[i];
-    for (int k = 1; k < n; ++k) {
-      s1 += sum[i + k * width];
-      q1 += sq[i + k * width];
-    }
-    const float d = s1 * inv;
-    sq[i] = gn_m2(q1 - d * s1);
-    sum[i] = d;
-  }
-  __syncthreads();
-  if (slot == 0) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sum[c + i] += pivot[i];
-  }
-  __syncthreads();
-  // and of each group: eight lanes each
-  const int cg = a.C / a.G, lane = threadIdx.x & 7;
-  const float icg = 1.0f / (float)cg;
+  // each group's channels and slots, by eight lanes
+  const float count = (float)(hi - lo) * (float)cg, inv = 1.0f / count;
   for (int g0 = 4 * (threadIdx.x >> 5); g0 < a.G; g0 += blockDim.x >> 3) {     // uniform over a warp
-    const int g = min(g0 + ((threadIdx.x >> 3) & 3), a.G - 1);
-    const float base = sum[g * cg];
-    float m = 0.0f, m2 = 0.0f, e2 = 0.0f;
-    for (int i = lane; i < cg; i += 8) {
-      const float e = sum[g * cg + i] - base;
-      m += e;
-      e2 = fmaf(e, e, e2);
-      m2 += sq[g * cg + i];
+    const int g = min(g0 + (lane >> 3), a.G - 1);
+    const float pivot = Elem<T>::to_f32(X[(int64_t)lo * a.ldx + g * cg]);
+    float s1 = 0.0f, q1 = 0.0f;
+    for (int i = g * cg + (lane & 7); i < (g + 1) * cg; i += 8) {
+      float s[8], q[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        s[k] = k < n ? sum[i + k * width] : 0.0f;
+        q[k] = k < n ? sq[i + k * width] : 0.0f;
+      }
+      s1 += ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
+      q1 += ((q[0] + q[1]) + (q[2] + q[3])) + ((q[4] + q[5]) + (q[6] + q[7]));
     }
 #pragma unroll
     for (int o = 4; o; o >>= 1) {
-      m += __shfl_xor_sync(0xFFFFFFFFu, m, o);
-      e2 += __shfl_xor_sync(0xFFFFFFFFu, e2, o);
-      m2 += __shfl_xor_sync(0xFFFFFFFFu, m2, o);
+      s1 += __shfl_xor_sync(0xFFFFFFFFu, s1, o);
+      q1 += __shfl_xor_sync(0xFFFFFFFFu, q1, o);
     }
-    m *= icg;
-    if (lane == 0 && g0 + ((threadIdx.x >> 3) & 3) < a.G)
-      a.part[(int64_t)blockIdx.x * a.G + g] = make_float2(base + m, m2 + rows * gn_m2(e2 - (float)cg * m * m));
+    if ((lane & 7) == 0 && g0 + (lane >> 3) < a.G) {
+      const float d = s1 * inv;
+      out[g] = make_float2(pivot + d, gn_m2(q1 - d * s1));
+    }
   }
 }
 
-// (mean, M2) of one group over the P blocks of its sample: `part` is block 0's entry, `lanes` lanes of a warp
-// work together (a power of two, `lane` among them); a block has `rows` of the S rows, the last what is left.
-SVDQ_DEV float2 gn_merge(const float2* part, int G, int P, int rows, int S, int cg, int lane, int lanes) {
-  const float base = part[0].x;
-  float n = 0.0f, m = 0.0f, m2 = 0.0f, e2 = 0.0f;
-#pragma unroll 8
-  for (int p = lane; p < P; p += lanes) {
-    const float2 v = part[(int64_t)p * G];
-    const float k = (float)min(rows, S - p * rows) * (float)cg;
+// Running merge of blocks' (n, mean, M2) against a common base: n, sum n (mean - base), sum n (mean - base)^2, M2.
+struct GnMerge {
+  float n = 0.0f, m = 0.0f, e2 = 0.0f, m2 = 0.0f;
+  SVDQ_DEV void add(float2 v, float base, float k) {
     const float e = v.x - base;
     n += k;
     m = fmaf(k, e, m);
     e2 = fmaf(k * e, e, e2);
     m2 += v.y;
   }
-  for (int o = lanes >> 1; o; o >>= 1) {
-    n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
-    m += __shfl_xor_sync(0xFFFFFFFFu, m, o);
-    e2 += __shfl_xor_sync(0xFFFFFFFFu, e2, o);
-    m2 += __shfl_xor_sync(0xFFFFFFFFu, m2, o);
+  // mean and 1 / sqrt(var + eps)
+  SVDQ_DEV float2 result(float base, float eps) const {
+    const float d = m / n;
+    return make_float2(base + d, __frsqrt_rn((m2 + gn_m2(e2 - d * m)) / n + eps));
   }
-  m /= n;
-  return make_float2(base + m, (m2 + gn_m2(e2 - n * m * m)) / n);      // mean, variance
+};
+
+// y / (1 + exp(-y)), two elements sharing a reciprocal, 1 / d0 = d1 / (d0 d1): three special-function operations a
+// pair instead of four, which bound the pass (16 a cycle and SM).  exp(-y) is cut at y = -40, where the result is
+// below 2e-16 in magnitude either way, so that the product of two d stays in range.
+SVDQ_DEV float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+SVDQ_DEV float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+SVDQ_DEV float2 silu_f32x2(float2 y) {
+  const float2 d = add_f32x2(make_float2(ex2(-1.44269504f * fmaxf(y.x, -40.0f)), ex2(-1.44269504f * fmaxf(y.y, -40.0f))),
+                             f2(1.0f));
+  const float r = rcp(d.x * d.y);
+  return mul_f32x2(y, mul_f32x2(f2(r), make_float2(d.y, d.x)));
 }
 
 SVDQ_DEV void gn_act(float (&y)[8], int act) {
-  if (act == ACT_SILU) {
+  if (act == ACT_NONE) return;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = __fdividef(y[i], 1.0f + __expf(-y[i]));
-  } else if (act == ACT_GELU) {
-#pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      const float2 g = gelu_f32x2(make_float2(y[i], y[i + 1]));
-      y[i] = g.x;
-      y[i + 1] = g.y;
-    }
+  for (int i = 0; i < 8; i += 2) {
+    const float2 v = make_float2(y[i], y[i + 1]), g = act == ACT_SILU ? silu_f32x2(v) : gelu_f32x2(v);
+    y[i] = g.x;
+    y[i + 1] = g.y;
   }
 }
 
-// The second pass.  QUANT: instead of Y, rows of 8-bit codes and their scales; a row's maximum is taken over the
-// lanes of a warp that hold it and joined through shared memory (integer maximum: any order), GN_QROWS rows a
-// thread at a time with one barrier.
-template <typename T, bool VEC, bool QUANT>
-__global__ void __launch_bounds__(GN_MAX_THREADS) k_group_apply(const GroupNormArgs a) {
-  constexpr int W = Elem<T>::kWords, U = QUANT ? GN_QROWS : GN_UNROLL<T>;
-  extern __shared__ float2 stat[];                       // G of (mean, rstd); QUANT: then 3 x GN_QROWS rp row maxima
-  const int b = blockIdx.x / a.P, p = blockIdx.x % a.P;
-  const int lo = p * a.rows, hi = min(a.S, lo + a.rows);
-  const int slot = threadIdx.x / a.nv, v = threadIdx.x % a.nv, c = 8 * v;
-  const int cg = a.C / a.G, lane = threadIdx.x & 31;
-  const bool work = slot < a.rp;
-  uint32_t* top = reinterpret_cast<uint32_t*>(stat + a.G);
-  const int per = U * a.rp;
-  if (QUANT)
-    for (int i = threadIdx.x; i < per; i += blockDim.x) top[i] = 0u;
-  float ga[8], be[8], mu[8], is[8];
-  if (work) {
-    gn_params<VEC>(a.gamma, 1.0f, c, a.C, ga);
-    gn_params<VEC>(a.beta, 0.0f, c, a.C, be);
-    gn_params<VEC>(QUANT ? a.inv_s : nullptr, 1.0f, c, a.C, is);
+// A thread's part of the second pass, set up before the statistics are there: its place (l2 threads a row), the
+// parameters of its channels, and its first rows (not where they are in shared memory).
+template <typename T, bool VEC, bool QUANT, bool KEEP>
+struct GnApply {
+  static constexpr int W = Elem<T>::kWords, U = GN_UNROLL<T>;
+  int slot, v, c;
+  bool on;
+  float ga[8], be[8], is[QUANT ? 8 : 1];
+  uint32_t x[U][W], nx[U][W];
+
+  SVDQ_DEV GnApply(const GroupNormArgs& a) {
+    slot = threadIdx.x / a.l2;
+    v = threadIdx.x - slot * a.l2;
+    c = 8 * v;
+    on = slot < a.rp2 && v < a.nv;
+    if (on) {
+      gn_params<VEC>(a.gamma, 1.0f, c, a.C, ga);
+      gn_params<VEC>(a.beta, 0.0f, c, a.C, be);
+      if constexpr (QUANT) gn_params<VEC>(a.inv_s, 1.0f, c, a.C, is);
+    }
   }
-  griddep_wait();
-  griddep_launch_dependents();
-  // 8 lanes a group: a warp merges four groups at a time
-  const float2* part = a.part + (int64_t)b * a.parts * a.G;
-  for (int g0 = 4 * (threadIdx.x >> 5); g0 < a.G; g0 += 4 * (blockDim.x >> 5)) {
-    const int g = g0 + (lane >> 3);
-    const float2 st = gn_merge(part + min(g, a.G - 1), a.G, a.parts, a.part_rows, a.S, cg, lane & 7, 8);
-    if (g < a.G && (lane & 7) == 0) stat[g] = make_float2(st.x, __frsqrt_rn(st.y + a.eps));
+  SVDQ_DEV void fetch(const GroupNormArgs& a, const T* X, const uint4* kept, int lo, int r0, uint32_t (&x)[U][W]) {
+    if (!on) return;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 - u * a.rp2 - slot;
+      if (r < lo) continue;
+      if constexpr (KEEP) {
+        const uint4* k = kept + ((r - lo) * a.nv + v) * (W / 4);
+#pragma unroll
+        for (int i = 0; i < W / 4; ++i) {
+          const uint4 d = k[i];
+          x[u][4 * i] = d.x;
+          x[u][4 * i + 1] = d.y;
+          x[u][4 * i + 2] = d.z;
+          x[u][4 * i + 3] = d.w;
+        }
+      } else {
+        gn_load<T, VEC>(X + (int64_t)r * a.ldx, c, a.C, x[u]);
+      }
+    }
   }
-  __syncthreads();
-  if (work) {
-    int g = c / cg, left = cg - c % cg;                  // the vector's channels, group by group
+};
+
+// Second pass over rows lo..hi of sample b, from the last to the first (t.fetch has the first step's rows).  stat:
+// (mean, rstd) of the groups; KEEP: the rows are in `kept`.  QUANT: instead of Y, rows of 8-bit codes and their
+// scales.  A row's l2 threads are whole warps, or 2^k <= 32 lanes of one: its maximum is a reduction over lanes, and
+// over warps through `top` (two buffers of U words a warp; one barrier a step).
+template <typename T, bool VEC, bool QUANT, bool KEEP>
+SVDQ_DEV void gn_apply_rows(const GroupNormArgs& a, GnApply<T, VEC, QUANT, KEEP>& t, const T* X, int b, int lo, int hi,
+                            const float2* stat, const uint4* kept, uint32_t* top) {
+  constexpr int W = Elem<T>::kWords, U = GN_UNROLL<T>;
+  const int slot = t.slot, v = t.v, c = t.c, cg = a.C / a.G, lane = threadIdx.x & 31;
+  const bool on = t.on;
+  float mu[8];
+  if (on) {
+    int g = c / cg, left = cg * (g + 1) - c;             // the vector's channels, group by group
     float2 st = stat[g];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -273,38 +308,28 @@ __global__ void __launch_bounds__(GN_MAX_THREADS) k_group_apply(const GroupNormA
       }
       --left;
       mu[i] = st.x;
-      ga[i] *= st.y;
+      t.ga[i] *= st.y;
     }
   }
-  const T* X = static_cast<const T*>(a.X) + (int64_t)b * a.S * a.ldx;
   T* Y = static_cast<T*>(a.Y) + (QUANT ? 0 : (int64_t)b * a.S * a.ldy);
   const auto value = [&](const uint32_t(&w)[W], float(&y)[8]) {
     Elem<T>::unpack(w, y);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = fmaf(y[i] - mu[i], ga[i], be[i]);
+    for (int i = 0; i < 8; ++i) y[i] = fmaf(y[i] - mu[i], t.ga[i], t.be[i]);
     gn_act(y, a.act);
   };
-  // lanes of this warp that hold the same row as this one
-  const uint32_t mates = QUANT ? __match_any_sync(0xFFFFFFFFu, slot) : 0u;
+  const int nw = a.l2 >> 5;                              // warps a row, 0: part of one
   int buf = 0;
-  // rows from the last to the first, U a thread at a time (uniform over the block)
-  for (int r0 = hi - 1; r0 >= lo; r0 -= per) {
-    uint32_t x[U][W];
-    if (work) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int r = r0 - u * a.rp - slot;
-        if (r >= lo) gn_load<T, VEC>(X + (int64_t)r * a.ldx, c, a.C, x[u]);
-      }
-    }
+  for (int r0 = hi - 1; r0 >= lo; r0 -= U * a.rp2) {     // uniform over the block
+    if (!KEEP) t.fetch(a, X, kept, lo, r0 - U * a.rp2, t.nx);
     if constexpr (!QUANT) {
-      if (work) {
+      if (on) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const int r = r0 - u * a.rp - slot;
+          const int r = r0 - u * a.rp2 - slot;
           if (r < lo) continue;
           float y[8];
-          value(x[u], y);
+          value(t.x[u], y);
           T* out = Y + (int64_t)r * a.ldy + c;
           if constexpr (VEC) {
             uint32_t o[W];
@@ -323,33 +348,49 @@ __global__ void __launch_bounds__(GN_MAX_THREADS) k_group_apply(const GroupNormA
         }
       }
     } else {
-      // Maxima of this step in buffer buf; the next step's buffer is cleared here, two barriers after its last use.
-      uint32_t* now = top + buf * per;
-      const int nb = buf == 2 ? 0 : buf + 1;
-      for (int i = threadIdx.x; i < per; i += blockDim.x) top[nb * per + i] = 0u;
       float y[U][8];
+      uint32_t m[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int r = r0 - u * a.rp - slot;
-        uint32_t m = 0u;
-        if (work && r >= lo) {
-          value(x[u], y[u]);
+        m[u] = 0u;
+        if (on && r0 - u * a.rp2 - slot >= lo) {
+          value(t.x[u], y[u]);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            y[u][i] = __fmul_rn(y[u][i], is[i]);
-            m = umax(m, abs_bits(y[u][i]));                  // C % 16 == 0: whole vectors
+            y[u][i] = __fmul_rn(y[u][i], t.is[i]);
+            m[u] = umax(m[u], abs_bits(y[u][i]));        // C % 16 == 0: whole vectors
           }
         }
-        m = __reduce_max_sync(mates, m);
-        if (work && r >= lo && lane == __ffs(mates) - 1) atomicMax(now + u * a.rp + slot, m);
       }
-      __syncthreads();
+      __syncwarp();                                      // the lanes parted above
+      if (nw) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) m[u] = __reduce_max_sync(0xFFFFFFFFu, m[u]);
+      } else {
+        for (int o = a.l2 >> 1; o; o >>= 1)
+#pragma unroll
+          for (int u = 0; u < U; ++u) m[u] = umax(m[u], __shfl_xor_sync(0xFFFFFFFFu, m[u], o));
+      }
+      if (nw > 1) {
+        uint32_t* now = top + buf * U * (blockDim.x >> 5);           // [u][warp]
+        const int warp = threadIdx.x >> 5;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (lane == u) now[u * (blockDim.x >> 5) + warp] = m[u];
+        __syncthreads();
+        if (slot < a.rp2) {
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            for (int k = 0; k < nw; ++k) m[u] = umax(m[u], now[u * (blockDim.x >> 5) + slot * nw + k]);
+        }
+        buf ^= 1;
+      }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int r = r0 - u * a.rp - slot;
-        if (work && r >= lo) {
+        const int r = r0 - u * a.rp2 - slot;
+        if (on && r >= lo) {
           float scale, mul;
-          i8_scale(now[u * a.rp + slot], scale, mul);
+          i8_scale(m[u], scale, mul);
           const int64_t row = (int64_t)b * a.S + r;
           if (v == 0) a.sx[row] = scale;
           const float one[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
@@ -357,20 +398,138 @@ __global__ void __launch_bounds__(GN_MAX_THREADS) k_group_apply(const GroupNormA
           *reinterpret_cast<uint2*>(a.Xq + row * a.C + c) = mul == 0.0f ? make_uint2(0u, 0u) : code;
         }
       }
-      buf = nb;
+    }
+    if (KEEP) {
+      t.fetch(a, X, kept, lo, r0 - U * a.rp2, t.x);
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < W; ++i) t.x[u][i] = t.nx[u][i];
     }
   }
 }
 
-// Where a sample has many blocks and many groups: their partials merged once, to one entry per group, which the
-// second pass then reads as a single block's.  A warp per (sample, group).
-__global__ void __launch_bounds__(256) k_group_merge(const float2* part, int64_t BG, int G, int P, int rows, int S,
-                                                     int cg, float2* out) {
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(GN_MAX_THREADS, 1) k_group_stats(const GroupNormArgs a) {
+  __shared__ __align__(16) float sum[GN_MAX_C], sq[GN_MAX_C];
   griddep_wait();
-  const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (i >= BG) return;
-  const float2 st = gn_merge(part + i / G * P * G + i % G, G, P, rows, S, cg, threadIdx.x & 31, 32);
-  if ((threadIdx.x & 31) == 0) out[i] = make_float2(st.x, st.y * ((float)S * (float)cg));
+  griddep_launch_dependents();
+  const int b = blockIdx.x / a.P, p = blockIdx.x - b * a.P;
+  const int lo = p * a.rows, hi = min(a.S, lo + a.rows);
+  gn_block_stats<T, VEC, false>(a, static_cast<const T*>(a.X) + (int64_t)b * a.S * a.ldx, lo, hi, sum, sq, nullptr,
+                                a.part + (int64_t)blockIdx.x * a.G);
+}
+
+// The sample's P partials of each group are merged by strips of threads: thread (j, g) takes every J-th block, ten
+// loads in flight, and the strips are joined through shared memory.
+constexpr int GN_MERGE_LOADS = 10;
+template <typename T, bool VEC, bool QUANT>
+__global__ void __launch_bounds__(GN_MAX_THREADS, 1) k_group_apply(const GroupNormArgs a) {
+  extern __shared__ __align__(16) float2 stat[];         // G of (mean, rstd), then a GnMerge a thread
+  __shared__ uint32_t top[2 * GN_UNROLL<T> * GN_MAX_THREADS / 32];
+  const int b = blockIdx.x / a.P, p = blockIdx.x - b * a.P;
+  const int lo = p * a.rows, hi = min(a.S, lo + a.rows);
+  const float cg = (float)(a.C / a.G);
+  GnMerge* strip = reinterpret_cast<GnMerge*>(stat + (a.G + 1) / 2 * 2);
+  const T* X = static_cast<const T*>(a.X) + (int64_t)b * a.S * a.ldx;
+  // Inputs may be read before the wait: the first pass started after everything before it was done.
+  GnApply<T, VEC, QUANT, false> t(a);
+  t.fetch(a, X, nullptr, lo, hi - 1, t.x);
+  griddep_wait();
+  griddep_launch_dependents();
+  const float2* part = a.part + (int64_t)b * a.P * a.G;
+  const int J = max(1, (int)blockDim.x / a.G), j = threadIdx.x / a.G, last_rows = a.S - (a.P - 1) * a.rows;
+  for (int g0 = 0; g0 < a.G; g0 += blockDim.x) {         // one round unless there are more groups than threads
+    const int g = g0 + (J > 1 ? threadIdx.x - j * a.G : threadIdx.x);
+    GnMerge acc;
+    if ((J > 1 ? j < J : true) && g < a.G) {
+      const float base = part[g].x;
+      for (int p0 = J > 1 ? j : 0; p0 < a.P; p0 += GN_MERGE_LOADS * J) {
+        float2 v[GN_MERGE_LOADS];
+#pragma unroll
+        for (int k = 0; k < GN_MERGE_LOADS; ++k)
+          if (p0 + k * J < a.P) v[k] = part[(int64_t)(p0 + k * J) * a.G + g];
+#pragma unroll
+        for (int k = 0; k < GN_MERGE_LOADS; ++k)
+          if (p0 + k * J < a.P) acc.add(v[k], base, cg * (float)(p0 + k * J == a.P - 1 ? last_rows : a.rows));
+      }
+      if (J == 1) stat[g] = acc.result(base, a.eps);
+      else strip[j * a.G + g] = acc;
+    }
+  }
+  if (J > 1) {
+    int n = J;
+    for (; n > 8;) {
+      const int h = (n + 1) >> 1;
+      __syncthreads();
+      for (int i = threadIdx.x; i < (n - h) * a.G; i += blockDim.x) {
+        strip[i].n += strip[i + h * a.G].n;
+        strip[i].m += strip[i + h * a.G].m;
+        strip[i].e2 += strip[i + h * a.G].e2;
+        strip[i].m2 += strip[i + h * a.G].m2;
+      }
+      n = h;
+    }
+    __syncthreads();
+    if (threadIdx.x < a.G) {
+      GnMerge acc = strip[threadIdx.x];
+#pragma unroll
+      for (int k = 1; k < 8; ++k)
+        if (k < n) {
+          const GnMerge o = strip[k * a.G + threadIdx.x];
+          acc.n += o.n;
+          acc.m += o.m;
+          acc.e2 += o.e2;
+          acc.m2 += o.m2;
+        }
+      stat[threadIdx.x] = acc.result(part[threadIdx.x].x, a.eps);
+    }
+  }
+  __syncthreads();
+  gn_apply_rows<T, VEC, QUANT, false>(a, t, X, b, lo, hi, stat, nullptr, top);
+}
+
+// Floats of k_group_norm's shared memory before the kept rows: own partials and statistics of G groups, sums and
+// squares of 8 values a thread (a multiple of 4).
+__host__ __device__ constexpr int gn_fixed_floats(int G, int threads) { return (4 * G + 16 * threads + 3) / 4 * 4; }
+
+template <typename T, bool VEC, bool QUANT>
+__global__ void __launch_bounds__(GN_MAX_THREADS, 1) k_group_norm(const GroupNormArgs a) {
+  extern __shared__ __align__(16) float gn_smem[];
+  __shared__ uint32_t top[2 * GN_UNROLL<T> * GN_MAX_THREADS / 32];
+  float* sum = gn_smem;
+  float* sq = sum + 8 * blockDim.x;
+  float2* mine = reinterpret_cast<float2*>(sq + 8 * blockDim.x);
+  float2* stat = mine + a.G;
+  uint4* kept = reinterpret_cast<uint4*>(gn_smem + gn_fixed_floats(a.G, blockDim.x));
+  griddep_wait();
+  griddep_launch_dependents();
+  const int b = blockIdx.x / a.P, p = blockIdx.x - b * a.P;
+  const int lo = p * a.rows, hi = min(a.S, lo + a.rows);
+  const T* X = static_cast<const T*>(a.X) + (int64_t)b * a.S * a.ldx;
+  gn_block_stats<T, VEC, true>(a, X, lo, hi, sum, sq, kept, mine);
+  GnApply<T, VEC, QUANT, true> t(a);                     // its loads on their way while the blocks meet
+  __syncwarp();
+  if (a.P > 1) cluster_sync_all();
+  else __syncthreads();
+  const float cg = (float)(a.C / a.G);
+  for (int g = threadIdx.x; g < a.G; g += blockDim.x) {
+    float2 v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < a.P) v[k] = a.P > 1 ? ld_cluster_f2(map_to_rank(smem_u32(mine + g), (uint32_t)k)) : mine[g];
+    GnMerge acc;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < a.P) acc.add(v[k], v[0].x, cg * (float)min(a.rows, a.S - k * a.rows));
+    stat[g] = acc.result(v[0].x, a.eps);
+  }
+  __syncwarp();
+  if (a.P > 1) cluster_sync_all();                       // no block leaves while another reads its partials
+  else __syncthreads();
+  t.fetch(a, X, kept, lo, hi - 1, t.x);
+  gn_apply_rows<T, VEC, QUANT, true>(a, t, X, b, lo, hi, stat, kept, top);
 }
 
 }  // namespace svdq

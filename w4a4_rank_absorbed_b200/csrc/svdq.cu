@@ -623,30 +623,57 @@ svdq_status launch_linear_i8(int dev, DevInfo* d, const int8_t* Xq, const float*
 // ------------------------------------------------------------- group norm ---
 constexpr int64_t kMaxNormC = GN_MAX_C;
 
-constexpr int64_t kNormBlocks = 148;      // blocks at work at one time: one an SM of a B200
-constexpr int64_t kNormMerge = 8192;      // partial entries a sample above which a launch of its own merges them
+constexpr int64_t kNormBlocks = 148;      // one block an SM of a B200
+constexpr int kNormSmem = 232448 - 2048;  // dynamic shared memory of k_group_norm, at most
 
 struct NormPlan {
-  int nv, rp, threads, P, rows;
-  bool merge;
+  bool one;                 // k_group_norm; else k_group_stats and k_group_apply
+  int nv, rp1, l2, rp2, threads1, threads2, P, rows;
 };
-// Rows are dealt to as many blocks as the GPU holds at one time, over all samples, as long as each thread keeps
-// about four rows (fewer leave a block nothing to have in flight).
-NormPlan plan_norm(int64_t B, int64_t S, int64_t C, int64_t G) {
+NormPlan plan_norm(int64_t B, int64_t S, int64_t C, int64_t G, int row_bytes, bool quant) {
   NormPlan p;
   p.nv = (int)((C + 7) / 8);
-  p.rp = (int)std::min<int64_t>(std::max(1, GN_MAX_THREADS / p.nv), S);
-  p.threads = (p.nv * p.rp + 31) / 32 * 32;
-  p.P = (int)std::max<int64_t>(1, std::min<int64_t>(kNormBlocks / B, S / (p.rp * 4)));
-  p.rows = (int)((S + p.P - 1) / p.P);
-  p.P = (int)((S + p.rows - 1) / p.rows);
-  p.merge = (int64_t)p.P * G > kNormMerge;
+  p.l2 = p.nv;
+  if (quant) {                            // whole warps a row, or a power of two of lanes
+    if (p.nv > 32) p.l2 = (p.nv + 31) / 32 * 32;
+    else for (p.l2 = 1; p.l2 < p.nv;) p.l2 *= 2;
+  }
+  const auto split = [&](int64_t blocks) {
+    p.P = (int)std::max<int64_t>(1, blocks);
+    p.rows = (int)((S + p.P - 1) / p.P);
+    p.P = (int)((S + p.rows - 1) / p.rows);
+    p.rp1 = std::min(std::max(1, GN_MAX_THREADS / p.nv), p.rows);
+    p.rp2 = std::min(std::max(1, GN_MAX_THREADS / p.l2), p.rows);
+    p.threads1 = (p.nv * p.rp1 + 31) / 32 * 32;
+    p.threads2 = (p.l2 * p.rp2 + 31) / 32 * 32;
+  };
+  const int64_t step = std::max(1, GN_MAX_THREADS / p.nv);         // rows a block takes at a time
+  // One launch where a cluster of up to eight blocks holds a sample, at least two steps a block.  Where the samples alone
+  // do not fill the GPU, only up to 64 KB a block: above that the many blocks of two launches win.
+  int64_t P = 1;
+  while (P < 8 && S >= 4 * P * step) P *= 2;
+  split(P);
+  const int threads = std::max(p.threads1, p.threads2);
+  const int64_t held = (int64_t)p.rows * row_bytes, room = kNormSmem - 4 * gn_fixed_floats((int)G, threads);
+  p.one = held <= room && (held <= (64 << 10) || B * p.P >= kNormBlocks);
+  if (p.one) {
+    p.threads1 = p.threads2 = threads;
+    return p;
+  }
+  // Otherwise as many blocks as the GPU holds at one time, over all samples, with about four rows a thread, and no
+  // more than keep a sample's partials few enough for every block to merge them.
+  split(std::min<int64_t>({kNormBlocks / B, S / (4 * step), 16384 / G}));
   return p;
 }
 
 size_t group_norm_workspace(int64_t B, int64_t S, int64_t C, int64_t G) {
-  const NormPlan p = plan_norm(B, S, C, G);
-  return (size_t)B * (size_t)G * (size_t)(p.P + (p.merge ? 1 : 0)) * sizeof(float2);
+  size_t need = 16;
+  for (int bytes = 2; bytes <= 4; bytes += 2)
+    for (int quant = 0; quant < 2; ++quant) {
+      const NormPlan p = plan_norm(B, S, C, G, (int)((C + 7) / 8) * 8 * bytes, quant != 0);
+      if (!p.one) need = std::max(need, (size_t)B * (size_t)G * (size_t)p.P * sizeof(float2));
+    }
+  return need;
 }
 
 struct NormArgs {
@@ -666,8 +693,9 @@ struct NormArgs {
 };
 
 template <typename T, bool VEC, bool QUANT>
-svdq_status launch_norm(const NormArgs& n, cudaStream_t s) {
-  const NormPlan p = plan_norm(n.B, n.S, n.C, n.G);
+svdq_status launch_norm(int dev, const NormArgs& n, cudaStream_t s) {
+  const int row_bytes = (int)((n.C + 7) / 8) * Elem<T>::kWords * 4;
+  const NormPlan p = plan_norm(n.B, n.S, n.C, n.G, row_bytes, QUANT);
   GroupNormArgs a;
   a.X = n.X;
   a.ldx = n.ldx;
@@ -675,43 +703,44 @@ svdq_status launch_norm(const NormArgs& n, cudaStream_t s) {
   a.C = (int)n.C;
   a.G = (int)n.G;
   a.nv = p.nv;
-  a.rp = p.rp;
+  a.rp1 = p.rp1;
+  a.l2 = p.l2;
+  a.rp2 = p.rp2;
   a.P = p.P;
-  a.rows = a.part_rows = p.rows;
-  a.parts = p.P;
+  a.rows = p.rows;
   a.part = static_cast<float2*>(n.ws);
   a.gamma = n.gamma;
   a.beta = n.beta;
   a.eps = n.eps;
   a.act = n.act;
-  a.streaming = (int64_t)n.B * n.S * n.C * (int64_t)sizeof(T) > (int64_t(48) << 20);
+  a.streaming = n.B * n.S * n.C * (int64_t)sizeof(T) > (int64_t(48) << 20);
   a.Y = n.Y;
   a.ldy = n.ldy;
   a.inv_s = n.inv_s;
   a.Xq = n.Xq;
   a.sx = n.sx;
   const int64_t blocks = n.B * p.P;
-  if (launch_pdl(k_group_stats<T, VEC>, dim3((unsigned)blocks), dim3(p.threads), 0, s, 1, a) != cudaSuccess)
-    return SVDQ_ERR_CUDA;
-  if (p.merge) {
-    const int64_t bg = n.B * n.G;
-    float2* merged = a.part + bg * p.P;
-    if (launch_pdl(k_group_merge, dim3((unsigned)((bg + 7) / 8)), dim3(256), 0, s, 1, (const float2*)a.part, bg, a.G, p.P,
-                   p.rows, a.S, a.C / a.G, merged) != cudaSuccess)
+  if (blocks > kMaxDim) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+  if (p.one) {
+    static std::atomic<bool> attr[kMaxDevices];
+    const svdq_status st = allow_smem(k_group_norm<T, VEC, QUANT>, dev, attr, kNormSmem);
+    if (st != SVDQ_OK) return st;
+    const size_t smem = (size_t)gn_fixed_floats(a.G, p.threads1) * 4 + (size_t)p.rows * (size_t)row_bytes;
+    if (launch_pdl(k_group_norm<T, VEC, QUANT>, dim3((unsigned)blocks), dim3(p.threads1), smem, s, p.P, a) != cudaSuccess)
       return SVDQ_ERR_CUDA;
-    a.part = merged;
-    a.parts = 1;
-    a.part_rows = a.S;
+    return launch_status();
   }
-  const size_t smem = (size_t)n.G * sizeof(float2) + (QUANT ? 3 * GN_QROWS * p.rp * sizeof(uint32_t) : 0);
-  if (launch_pdl(k_group_apply<T, VEC, QUANT>, dim3((unsigned)blocks), dim3(p.threads), smem, s, 1, a) != cudaSuccess)
+  if (launch_pdl(k_group_stats<T, VEC>, dim3((unsigned)blocks), dim3(p.threads1), 0, s, 1, a) != cudaSuccess)
+    return SVDQ_ERR_CUDA;
+  const size_t smem = ((size_t)n.G + 1) / 2 * 2 * sizeof(float2) + (size_t)p.threads2 * sizeof(GnMerge);
+  if (launch_pdl(k_group_apply<T, VEC, QUANT>, dim3((unsigned)blocks), dim3(p.threads2), smem, s, 1, a) != cudaSuccess)
     return SVDQ_ERR_CUDA;
   return launch_status();
 }
 template <typename T, bool QUANT>
-svdq_status launch_norm(const NormArgs& n, cudaStream_t s) {
+svdq_status launch_norm(int dev, const NormArgs& n, cudaStream_t s) {
   const bool vec = n.C % 8 == 0 && n.ldx * sizeof(T) % 16 == 0 && (QUANT || n.ldy * sizeof(T) % 16 == 0);
-  return vec ? launch_norm<T, true, QUANT>(n, s) : launch_norm<T, false, QUANT>(n, s);
+  return vec ? launch_norm<T, true, QUANT>(dev, n, s) : launch_norm<T, false, QUANT>(dev, n, s);
 }
 
 template <bool QUANT>
@@ -736,9 +765,9 @@ svdq_status norm_impl(const NormArgs& n, cudaStream_t s) {
   int dev;
   DevInfo* d;
   if ((st = current_device(&dev, &d)) != SVDQ_OK) return st;
-  if (n.type == SVDQ_BF16) return launch_norm<__nv_bfloat16, QUANT>(n, s);
-  if (n.type == SVDQ_FP16) return launch_norm<__half, QUANT>(n, s);
-  return launch_norm<float, QUANT>(n, s);
+  if (n.type == SVDQ_BF16) return launch_norm<__nv_bfloat16, QUANT>(dev, n, s);
+  if (n.type == SVDQ_FP16) return launch_norm<__half, QUANT>(dev, n, s);
+  return launch_norm<float, QUANT>(dev, n, s);
 }
 
 }  // namespace
