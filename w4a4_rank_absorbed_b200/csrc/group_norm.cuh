@@ -26,8 +26,12 @@ namespace svdq {
 
 enum : int { ACT_NONE = 0, ACT_SILU = 1, ACT_GELU = 2 };
 
-constexpr int GN_MAX_THREADS = 512;
-constexpr int GN_MAX_C = 8 * GN_MAX_THREADS;
+// Threads a block: 640 for large tensors, whose passes are bound by what is in flight (a megapixel of 128 channels: 149
+// us, 161 with 512), 512 for small ones, whose folds and merges are shorter with fewer rows at a time (64 rows of 320:
+// 6.7 us, 7.1 with 640), and where codes are made (their registers).
+constexpr int GN_MAX_THREADS = 640;
+constexpr int GN_SMALL_THREADS = 512;
+constexpr int GN_MAX_C = 8 * GN_SMALL_THREADS;
 // Rows a thread has in flight, 64 bytes of them.
 template <typename T>
 constexpr int GN_UNROLL = 8 / (int)sizeof(T);
@@ -412,7 +416,7 @@ SVDQ_DEV void gn_apply_rows(const GroupNormArgs& a, GnApply<T, VEC, QUANT, KEEP>
 
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(GN_MAX_THREADS, 1) k_group_stats(const GroupNormArgs a) {
-  __shared__ __align__(16) float sum[GN_MAX_C], sq[GN_MAX_C];
+  __shared__ __align__(16) float sum[8 * GN_MAX_THREADS], sq[8 * GN_MAX_THREADS];
   griddep_wait();
   griddep_launch_dependents();
   const int b = blockIdx.x / a.P, p = blockIdx.x - b * a.P;
@@ -425,7 +429,7 @@ __global__ void __launch_bounds__(GN_MAX_THREADS, 1) k_group_stats(const GroupNo
 // loads in flight, and the strips are joined through shared memory.
 constexpr int GN_MERGE_LOADS = 10;
 template <typename T, bool VEC, bool QUANT>
-__global__ void __launch_bounds__(GN_MAX_THREADS, 1) k_group_apply(const GroupNormArgs a) {
+__global__ void __launch_bounds__(QUANT ? GN_SMALL_THREADS : GN_MAX_THREADS, 1) k_group_apply(const GroupNormArgs a) {
   extern __shared__ __align__(16) float2 stat[];         // G of (mean, rstd), then a GnMerge a thread
   __shared__ uint32_t top[2 * GN_UNROLL<T> * GN_MAX_THREADS / 32];
   const int b = blockIdx.x / a.P, p = blockIdx.x - b * a.P;
@@ -495,7 +499,7 @@ __global__ void __launch_bounds__(GN_MAX_THREADS, 1) k_group_apply(const GroupNo
 __host__ __device__ constexpr int gn_fixed_floats(int G, int threads) { return (4 * G + 16 * threads + 3) / 4 * 4; }
 
 template <typename T, bool VEC, bool QUANT>
-__global__ void __launch_bounds__(GN_MAX_THREADS, 1) k_group_norm(const GroupNormArgs a) {
+__global__ void __launch_bounds__(GN_SMALL_THREADS, 1) k_group_norm(const GroupNormArgs a) {
   extern __shared__ __align__(16) float gn_smem[];
   __shared__ uint32_t top[2 * GN_UNROLL<T> * GN_MAX_THREADS / 32];
   float* sum = gn_smem;

@@ -638,21 +638,23 @@ NormPlan plan_norm(int64_t B, int64_t S, int64_t C, int64_t G, int row_bytes, bo
     if (p.nv > 32) p.l2 = (p.nv + 31) / 32 * 32;
     else for (p.l2 = 1; p.l2 < p.nv;) p.l2 *= 2;
   }
-  const auto split = [&](int64_t blocks) {
+  const bool large = !quant && B * S * row_bytes > (int64_t(16) << 20);
+  const int most = large ? GN_MAX_THREADS : GN_SMALL_THREADS;
+  const auto split = [&](int64_t blocks, int most) {
     p.P = (int)std::max<int64_t>(1, blocks);
     p.rows = (int)((S + p.P - 1) / p.P);
     p.P = (int)((S + p.rows - 1) / p.rows);
-    p.rp1 = std::min(std::max(1, GN_MAX_THREADS / p.nv), p.rows);
-    p.rp2 = std::min(std::max(1, GN_MAX_THREADS / p.l2), p.rows);
+    p.rp1 = std::min(std::max(1, most / p.nv), p.rows);
+    p.rp2 = std::min(std::max(1, most / p.l2), p.rows);
     p.threads1 = (p.nv * p.rp1 + 31) / 32 * 32;
     p.threads2 = (p.l2 * p.rp2 + 31) / 32 * 32;
   };
-  const int64_t step = std::max(1, GN_MAX_THREADS / p.nv);         // rows a block takes at a time
+  const int64_t step = std::max(1, GN_SMALL_THREADS / p.nv);       // rows a block takes at a time
   // One launch where a cluster of up to eight blocks holds a sample, at least two steps a block.  Where the samples alone
   // do not fill the GPU, only up to 64 KB a block: above that the many blocks of two launches win.
   int64_t P = 1;
   while (P < 8 && S >= 4 * P * step) P *= 2;
-  split(P);
+  split(P, GN_SMALL_THREADS);
   const int threads = std::max(p.threads1, p.threads2);
   const int64_t held = (int64_t)p.rows * row_bytes, room = kNormSmem - 4 * gn_fixed_floats((int)G, threads);
   p.one = held <= room && (held <= (64 << 10) || B * p.P >= kNormBlocks);
@@ -662,7 +664,7 @@ NormPlan plan_norm(int64_t B, int64_t S, int64_t C, int64_t G, int row_bytes, bo
   }
   // Otherwise as many blocks as the GPU holds at one time, over all samples, with about four rows a thread, and no
   // more than keep a sample's partials few enough for every block to merge them.
-  split(std::min<int64_t>({kNormBlocks / B, S / (4 * step), 16384 / G}));
+  split(std::min<int64_t>({kNormBlocks / B, S / (4 * step), 16384 / G}), most);
   return p;
 }
 
