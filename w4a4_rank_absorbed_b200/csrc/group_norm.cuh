@@ -32,9 +32,10 @@ enum : int { ACT_NONE = 0, ACT_SILU = 1, ACT_GELU = 2 };
 constexpr int GN_MAX_THREADS = 640;
 constexpr int GN_SMALL_THREADS = 512;
 constexpr int GN_MAX_C = 8 * GN_SMALL_THREADS;
-// Rows a thread has in flight, 64 bytes of them.
-template <typename T>
-constexpr int GN_UNROLL = 8 / (int)sizeof(T);
+// Rows a thread takes at a time (and as many on their way): 64 bytes of them; two where codes are made, whose values
+// wait in registers for their row's maximum (2 x 1024 x 1280: 10.2 us, 11.3 with four).
+template <typename T, bool QUANT>
+constexpr int GN_UNROLL = QUANT ? 2 : 8 / (int)sizeof(T);
 
 struct GroupNormArgs {
   const void* X;
@@ -105,7 +106,7 @@ SVDQ_DEV float gn_m2(float v) { return v < 0.0f ? 0.0f : v; }
 template <typename T, bool VEC, bool KEEP>
 SVDQ_DEV void gn_block_stats(const GroupNormArgs& a, const T* X, int lo, int hi, float* sum, float* sq, uint4* kept,
                              float2* out) {
-  constexpr int W = Elem<T>::kWords, U = GN_UNROLL<T>;
+  constexpr int W = Elem<T>::kWords, U = GN_UNROLL<T, false>;
   const int slot = threadIdx.x / a.nv, v = threadIdx.x - slot * a.nv, c = 8 * v;
   const int width = 8 * a.nv, cg = a.C / a.G, lane = threadIdx.x & 31;
   if (slot < a.rp1) {
@@ -250,7 +251,7 @@ SVDQ_DEV void gn_act(float (&y)[8], int act) {
 // parameters of its channels, and its first rows (not where they are in shared memory).
 template <typename T, bool VEC, bool QUANT, bool KEEP>
 struct GnApply {
-  static constexpr int W = Elem<T>::kWords, U = GN_UNROLL<T>;
+  static constexpr int W = Elem<T>::kWords, U = GN_UNROLL<T, QUANT>;
   int slot, v, c;
   bool on;
   float ga[8], be[8], is[QUANT ? 8 : 1];
@@ -292,12 +293,12 @@ struct GnApply {
 
 // Second pass over rows lo..hi of sample b, from the last to the first (t.fetch has the first step's rows).  stat:
 // (mean, rstd) of the groups; KEEP: the rows are in `kept`.  QUANT: instead of Y, rows of 8-bit codes and their
-// scales.  A row's l2 threads are whole warps, or 2^k <= 32 lanes of one: its maximum is a reduction over lanes, and
+// scales.  A row's l2 threads are whole warps, or 4 to 32 lanes of one, a power of two: its maximum is a reduction over lanes, and
 // over warps through `top` (two buffers of U words a warp; one barrier a step).
 template <typename T, bool VEC, bool QUANT, bool KEEP>
 SVDQ_DEV void gn_apply_rows(const GroupNormArgs& a, GnApply<T, VEC, QUANT, KEEP>& t, const T* X, int b, int lo, int hi,
                             const float2* stat, const uint4* kept, uint32_t* top) {
-  constexpr int W = Elem<T>::kWords, U = GN_UNROLL<T>;
+  constexpr int W = Elem<T>::kWords, U = GN_UNROLL<T, QUANT>;
   const int slot = t.slot, v = t.v, c = t.c, cg = a.C / a.G, lane = threadIdx.x & 31;
   const bool on = t.on;
   float mu[8];
@@ -389,17 +390,22 @@ SVDQ_DEV void gn_apply_rows(const GroupNormArgs& a, GnApply<T, VEC, QUANT, KEEP>
         }
         buf ^= 1;
       }
+      // lane j of a row's threads works out the scale of its row j of the U (two divisions), for all of them
+      const int group = min(a.l2, 32), j = lane & (group - 1);
+      uint32_t own = m[0];
+#pragma unroll
+      for (int u = 1; u < U; ++u) own = j == u ? m[u] : own;
+      float scale, mul;
+      i8_scale(own, scale, mul);
+      if (v < U && slot < a.rp2 && r0 - v * a.rp2 - slot >= lo) a.sx[(int64_t)b * a.S + r0 - v * a.rp2 - slot] = scale;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int r = r0 - u * a.rp2 - slot;
+        const float mu = __shfl_sync(0xFFFFFFFFu, mul, u, group);
         if (on && r >= lo) {
-          float scale, mul;
-          i8_scale(m[u], scale, mul);
-          const int64_t row = (int64_t)b * a.S + r;
-          if (v == 0) a.sx[row] = scale;
           const float one[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
-          const uint2 code = i8_codes(y[u], one, mul);
-          *reinterpret_cast<uint2*>(a.Xq + row * a.C + c) = mul == 0.0f ? make_uint2(0u, 0u) : code;
+          const uint2 code = i8_codes(y[u], one, mu);
+          *reinterpret_cast<uint2*>(a.Xq + ((int64_t)b * a.S + r) * a.C + c) = mu == 0.0f ? make_uint2(0u, 0u) : code;
         }
       }
     }
@@ -431,7 +437,7 @@ constexpr int GN_MERGE_LOADS = 10;
 template <typename T, bool VEC, bool QUANT>
 __global__ void __launch_bounds__(QUANT ? GN_SMALL_THREADS : GN_MAX_THREADS, 1) k_group_apply(const GroupNormArgs a) {
   extern __shared__ __align__(16) float2 stat[];         // G of (mean, rstd), then a GnMerge a thread
-  __shared__ uint32_t top[2 * GN_UNROLL<T> * GN_MAX_THREADS / 32];
+  __shared__ uint32_t top[2 * GN_UNROLL<T, QUANT> * GN_MAX_THREADS / 32];
   const int b = blockIdx.x / a.P, p = blockIdx.x - b * a.P;
   const int lo = p * a.rows, hi = min(a.S, lo + a.rows);
   const float cg = (float)(a.C / a.G);
@@ -501,7 +507,7 @@ __host__ __device__ constexpr int gn_fixed_floats(int G, int threads) { return (
 template <typename T, bool VEC, bool QUANT>
 __global__ void __launch_bounds__(GN_SMALL_THREADS, 1) k_group_norm(const GroupNormArgs a) {
   extern __shared__ __align__(16) float gn_smem[];
-  __shared__ uint32_t top[2 * GN_UNROLL<T> * GN_MAX_THREADS / 32];
+  __shared__ uint32_t top[2 * GN_UNROLL<T, QUANT> * GN_MAX_THREADS / 32];
   float* sum = gn_smem;
   float* sq = sum + 8 * blockDim.x;
   float2* mine = reinterpret_cast<float2*>(sq + 8 * blockDim.x);

@@ -634,9 +634,9 @@ NormPlan plan_norm(int64_t B, int64_t S, int64_t C, int64_t G, int row_bytes, bo
   NormPlan p;
   p.nv = (int)((C + 7) / 8);
   p.l2 = p.nv;
-  if (quant) {                            // whole warps a row, or a power of two of lanes
+  if (quant) {                            // whole warps a row, or a power of two of lanes, at least four
     if (p.nv > 32) p.l2 = (p.nv + 31) / 32 * 32;
-    else for (p.l2 = 1; p.l2 < p.nv;) p.l2 *= 2;
+    else for (p.l2 = 4; p.l2 < p.nv;) p.l2 *= 2;
   }
   const bool large = !quant && B * S * row_bytes > (int64_t(16) << 20);
   const int most = large ? GN_MAX_THREADS : GN_SMALL_THREADS;
