@@ -447,6 +447,22 @@ SVDQ_API svdq_status svdq_group_norm_quantize_i8(const void* X, int type, int64_
                                                  size_t workspace_bytes, svdq_stream_t stream);
 
 /*
+ * svdq_call -- one of the calls above with its arguments in an array, for
+ * bindings whose foreign-function calls cost by the argument (ctypes: about a
+ * quarter of a microsecond each).  args holds one 8-byte word per parameter of
+ * the entry point, in its order: pointers and sizes as they are, ints as
+ * int64_t, float eps as a double.  SVDQ_ERR_INVALID_ARG for another entry.
+ */
+typedef enum {
+    SVDQ_CALL_QUANTIZE_ACT_I8 = 0,
+    SVDQ_CALL_LINEAR_I8 = 1,
+    SVDQ_CALL_FORWARD_I8 = 2,
+    SVDQ_CALL_GROUP_NORM = 3,
+    SVDQ_CALL_GROUP_NORM_QUANTIZE_I8 = 4
+} svdq_entry;
+SVDQ_API svdq_status svdq_call(int entry, const void* args);
+
+/*
  * Calibration on the GPU ("From SmoothQuant to SVDQuant", quantization scheme:
  * the smoothing factors, the low-rank split and the activation global scale are
  * fixed offline from calibration data; section Smooth Quant (W8A8): the

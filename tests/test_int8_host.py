@@ -102,7 +102,7 @@ def test_rows_of_strided_tensors():
 
 def test_vectors_are_checked():
     t = torch.zeros(8)
-    assert C._vec(None, torch.float32, 8, -1, "t") is None
+    assert C._vec(None, torch.float32, 8, -1, "t") == 0
     assert C._vec(t, torch.float32, 8, -1, "t") == t.data_ptr()
     for bad, kind in ((t[::2], ValueError), (t[:7], ValueError), (t.double(), TypeError)):
         with pytest.raises(kind):
@@ -141,3 +141,36 @@ def test_calibration_smooths():
     keep = torch.arange(48) != 3
     assert torch.allclose(d.s[keep], want[keep])
     assert torch.allclose((X.double() * d.inv_s) @ d.W_hat.double(), X.double() @ W.double(), rtol=1e-5, atol=1e-5)
+
+
+def test_packed_calls_are_the_calls(lib):
+    """svdq_call unpacks each entry point's arguments in their order: the refusal of one changed argument at a time
+    is the entry point's own."""
+    import struct
+    for entry, name, base in ((C._quantize_act_i8, "svdq_quantize_act_i8", QUANT), (C._linear_i8, "svdq_linear_i8", LINEAR),
+                              (C._forward_i8, "svdq_forward_i8", FORWARD), (C._group_norm, "svdq_group_norm", NORM),
+                              (C._group_norm_quantize_i8, "svdq_group_norm_quantize_i8", NORMQ)):
+        seen = set()
+        for key, old in base.items():
+            for new in (None, -1, 3, 8, 1 << 40):
+                if key == "eps":
+                    new = -1.0 if new is None else float(new)
+                elif new is None and isinstance(old, int) and key[0].islower() and key not in ("ws", "sx", "sw", "inv_s",
+                                                                                            "gamma", "beta"):
+                    continue
+                elif new is None and key in "MNKBSCG":
+                    continue
+                elif new in (-1, 1 << 40) and key not in ("M", "N", "K", "B", "S", "C", "G", "ldx", "ldy"):
+                    continue
+                args = dict(base, **{key: new})
+                direct = _call(lib, name, base, **{key: new})
+                if direct in (C.SVDQ_OK, C.SVDQ_ERR_CUDA, C.SVDQ_ERR_DEVICE):
+                    continue                        # accepted: nothing to compare without a launch
+                seen.add((key, direct))
+                block = entry.pack(*[0 if v is None else v for v in args.values()], 0)
+                assert lib.svdq_call(entry.index, block) == direct, (name, key, new)
+        assert len(seen) >= 8
+    assert lib.svdq_call(5, b"\0" * 200) == INVAL and lib.svdq_call(-1, b"\0" * 200) == INVAL
+    assert lib.svdq_call(0, None) == INVAL
+    block = struct.pack("<16q", *([0] * 16))
+    assert lib.svdq_call(1, block) == INVAL

@@ -538,7 +538,7 @@ struct LinearI8Plan {
   bool pair;
   int nt, split;
 };
-LinearI8Plan plan_linear_i8(int64_t M, int64_t N, int64_t K, int sms) {
+LinearI8Plan find_plan_linear_i8(int64_t M, int64_t N, int64_t K, int sms) {
   const int64_t nkt = (K + 127) / 128;
   LinearI8Plan best = {true, 256, 1};
   double least = 1e30;
@@ -570,6 +570,23 @@ LinearI8Plan plan_linear_i8(int64_t M, int64_t N, int64_t K, int sms) {
     if (nt >= m16) break;
   }
   return best;
+}
+
+// The last plan of each calling thread is kept: a layer's calls are alike, and the search costs half a microsecond.
+LinearI8Plan plan_linear_i8(int64_t M, int64_t N, int64_t K, int sms) {
+  static thread_local struct {
+    int64_t M = 0, N = 0, K = 0;
+    int sms = 0;
+    LinearI8Plan plan;
+  } last;
+  if (last.M != M || last.N != N || last.K != K || last.sms != sms) {
+    last.plan = find_plan_linear_i8(M, N, K, sms);
+    last.M = M;
+    last.N = N;
+    last.K = K;
+    last.sms = sms;
+  }
+  return last.plan;
 }
 
 // w_early: the kernel before this one on the stream is a quantizer of this library, which has waited for
@@ -1021,6 +1038,45 @@ svdq_status svdq_group_norm_quantize_i8(const void* X, int type, int64_t ldx, in
   const NormArgs n = {X, type, ldx, B, S, C, G, gamma, beta, eps, act, nullptr, 0, inv_s, Xq, sx, workspace,
                       workspace_bytes};
   return norm_impl<true>(n, reinterpret_cast<cudaStream_t>(stream));
+}
+
+svdq_status svdq_call(int entry, const void* args) {
+  if (!args) return SVDQ_ERR_INVALID_ARG;
+  const unsigned char* words = static_cast<const unsigned char*>(args);   // at any alignment
+  const auto word = [&](int i) {
+    int64_t v;
+    std::memcpy(&v, words + 8 * i, 8);
+    return v;
+  };
+  const auto num = [&](int i) {              // an int parameter: a value outside its range is no valid argument
+    const int64_t v = word(i);
+    return v < INT32_MIN || v > INT32_MAX ? -1 : (int)v;
+  };
+  const auto real = [&](int i) {
+    double v;
+    std::memcpy(&v, words + 8 * i, 8);
+    return (float)v;
+  };
+  const auto p = [&](int i) { return reinterpret_cast<void*>(word(i)); };
+  const auto f = [&](int i) { return reinterpret_cast<float*>(word(i)); };
+  const auto q = [&](int i) { return reinterpret_cast<int8_t*>(word(i)); };
+  const auto stream = [&](int i) { return reinterpret_cast<svdq_stream_t>(word(i)); };
+  switch (entry) {
+    case SVDQ_CALL_QUANTIZE_ACT_I8:
+      return svdq_quantize_act_i8(p(0), num(1), word(2), word(3), word(4), f(5), q(6), f(7), stream(8));
+    case SVDQ_CALL_LINEAR_I8:
+      return svdq_linear_i8(q(0), f(1), q(2), f(3), f(4), p(5), num(6), word(7), word(8), word(9), word(10), stream(11));
+    case SVDQ_CALL_FORWARD_I8:
+      return svdq_forward_i8(p(0), num(1), word(2), f(3), q(4), f(5), f(6), p(7), num(8), word(9), word(10), word(11),
+                             word(12), p(13), (size_t)word(14), stream(15));
+    case SVDQ_CALL_GROUP_NORM:
+      return svdq_group_norm(p(0), num(1), word(2), word(3), word(4), word(5), word(6), f(7), f(8), real(9), num(10),
+                             p(11), word(12), p(13), (size_t)word(14), stream(15));
+    case SVDQ_CALL_GROUP_NORM_QUANTIZE_I8:
+      return svdq_group_norm_quantize_i8(p(0), num(1), word(2), word(3), word(4), word(5), word(6), f(7), f(8), real(9),
+                                         num(10), f(11), q(12), f(13), p(14), (size_t)word(15), stream(16));
+    default: return SVDQ_ERR_INVALID_ARG;
+  }
 }
 
 svdq_status svdq_calib_absmax_cols(const uint16_t* X, int64_t M, int64_t K, float* amax_x, int accumulate,

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -45,7 +46,7 @@ EXPORTED = ("svdq_status_string", "svdq_version", "svdq_sf_bytes", "svdq_pack_we
             "svdq_calib_absmax_cols", "svdq_calib_absmax_rows", "svdq_calib_smooth", "svdq_calib_scale_rows",
             "svdq_calib_act_amax", "svdq_map_cache_stats", "svdq_build_flags", "svdq_pack_weight_i8",
             "svdq_quantize_act_i8", "svdq_linear_i8", "svdq_forward_i8", "svdq_forward_i8_workspace_bytes",
-            "svdq_group_norm", "svdq_group_norm_workspace_bytes", "svdq_group_norm_quantize_i8")
+            "svdq_group_norm", "svdq_group_norm_workspace_bytes", "svdq_group_norm_quantize_i8", "svdq_call")
 
 SVDQ_BF16, SVDQ_FP32, SVDQ_FP16 = 0, 1, 2
 _DTYPES = {torch.bfloat16: SVDQ_BF16, torch.float32: SVDQ_FP32, torch.float16: SVDQ_FP16}
@@ -133,6 +134,8 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
                                                         _P, _Z, _P])):
         getattr(lib, name).restype = _I
         getattr(lib, name).argtypes = args
+    lib.svdq_call.restype = _I
+    lib.svdq_call.argtypes = [_I, ctypes.c_char_p]
     lib.svdq_forward_i8_workspace_bytes.restype = _Z
     lib.svdq_forward_i8_workspace_bytes.argtypes = [_I64, _I64]
     lib.svdq_group_norm_workspace_bytes.restype = _Z
@@ -401,19 +404,19 @@ def svdq_get_device_error(stream=None):
 # These calls launch on the device of their first tensor, on `stream` or torch's current stream of
 # that device; tensors on another device, too small or of another type are refused here, since the
 # library sees raw pointers only.
-def _vec(t, dtype, n: int, dev: int, name: str) -> Optional[int]:
-    """Pointer of a contiguous tensor of at least n elements (None passes: an argument left out)."""
+def _vec(t, dtype, n: int, dev: int, name: str) -> int:
+    """Pointer of a contiguous tensor of at least n elements (None, an argument left out: 0)."""
     if t is None:
-        return None
+        return 0
+    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.numel() >= n:
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError(f"{name}: expected dtype {dtype}, got {t.dtype}")
     if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous tensor")
-    if t.numel() < n:
-        raise ValueError(f"{name}: expected {n} elements, got {t.numel()}")
-    return t.data_ptr()
+    raise ValueError(f"{name}: expected {n} elements, got {t.numel()}")
 
 
 def _rows(t, rows: int, width: int, dev: int, name: str):
@@ -425,7 +428,7 @@ def _rows(t, rows: int, width: int, dev: int, name: str):
     if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
     shape = t.shape
-    if t.numel() != rows * width or not shape or shape[-1] != width:
+    if not shape or shape[-1] != width or t.numel() != rows * width:
         raise ValueError(f"{name}: expected {rows} rows of {width}, got {tuple(shape)}")
     if t.is_contiguous():
         return t.data_ptr(), ty, width
@@ -450,40 +453,68 @@ def _cuda_index(t, name: str) -> int:
     return t.get_device()
 
 
-def _call(name: str, dev: int, stream, *args) -> None:
-    fn = getattr(load_library(), name)
+# torch's current stream as a raw handle, without the Stream object around it (where this torch has it)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _on(stream, dev: int, where: str) -> int:
+    """The stream of a call whose tensors are on device `dev`."""
     if stream is None:
-        stream = torch.cuda.current_stream(dev).cuda_stream
-    elif isinstance(stream, torch.cuda.Stream):
+        return _raw_stream(dev)
+    if isinstance(stream, torch.cuda.Stream):
         if stream.device_index != dev:
-            raise ValueError(f"{name}: stream of cuda:{stream.device_index}, tensors on cuda:{dev}")
-        stream = stream.cuda_stream
-    if torch.cuda.current_device() == dev:
-        st = fn(*args, int(stream))
-    else:
-        with torch.cuda.device(dev):
-            st = fn(*args, int(stream))
-    if st != SVDQ_OK:
-        raise SVDQError(st, name)
+            raise ValueError(f"{where}: stream of cuda:{stream.device_index}, tensors on cuda:{dev}")
+        return stream.cuda_stream
+    return int(stream)
+
+
+class _Entry:
+    """An entry point called through svdq_call: its arguments packed into one array of 8-byte words (`form`: P a
+    pointer or handle, q an integer, d a float, the last one the stream)."""
+
+    def __init__(self, index: int, name: str, form: str):
+        self.index, self.name, self.pack = index, name, struct.Struct("<" + form.replace("P", "Q")).pack
+
+    def __call__(self, dev: int, stream, *args) -> None:
+        block = self.pack(*args, _on(stream, dev, self.name))
+        call = (_lib or load_library()).svdq_call
+        if torch.cuda.current_device() == dev:
+            st = call(self.index, block)
+        else:
+            with torch.cuda.device(dev):
+                st = call(self.index, block)
+        if st != SVDQ_OK:
+            raise SVDQError(st, self.name)
+
+
+_quantize_act_i8 = _Entry(0, "svdq_quantize_act_i8", "PqqqqPPPP")
+_linear_i8 = _Entry(1, "svdq_linear_i8", "PPPPPPqqqqqP")
+_forward_i8 = _Entry(2, "svdq_forward_i8", "PqqPPPPPqqqqqPqP")
+_group_norm = _Entry(3, "svdq_group_norm", "PqqqqqqPPdqPqPqP")
+_group_norm_quantize_i8 = _Entry(4, "svdq_group_norm_quantize_i8", "PqqqqqqPPdqPPPPqP")
 
 
 def svdq_pack_weight_i8(W_hat, K: int, N: int, Wq, sw, stream=None) -> None:
     d = _cuda_index(W_hat, "W_hat")
-    _call("svdq_pack_weight_i8", d, stream, _vec(W_hat, torch.float32, K * N, d, "W_hat"), K, N,
-          _vec(Wq, torch.int8, N * K, d, "Wq"), _vec(sw, torch.float32, N, d, "sw"))
+    with torch.cuda.device(d):
+        st = load_library().svdq_pack_weight_i8(_vec(W_hat, torch.float32, K * N, d, "W_hat"), K, N,
+                                                _vec(Wq, torch.int8, N * K, d, "Wq"), _vec(sw, torch.float32, N, d, "sw"),
+                                                _on(stream, d, "svdq_pack_weight_i8"))
+    _check(st, "svdq_pack_weight_i8")
 
 
 def svdq_quantize_act_i8(X, M: int, K: int, inv_s, Xq, sx, stream=None) -> None:
     d = _cuda_index(X, "X")
     x, xt, ldx = _rows(X, M, K, d, "X")
-    _call("svdq_quantize_act_i8", d, stream, x, xt, ldx, M, K, _vec(inv_s, torch.float32, K, d, "inv_s"),
+    _quantize_act_i8(d, stream, x, xt, ldx, M, K, _vec(inv_s, torch.float32, K, d, "inv_s"),
           _vec(Xq, torch.int8, M * K, d, "Xq"), _vec(sx, torch.float32, M, d, "sx"))
 
 
 def svdq_linear_i8(Xq, sx, Wq, sw, bias, Y, M: int, N: int, K: int, stream=None) -> None:
     d = _cuda_index(Xq, "Xq")
     y, yt, ldy = _rows(Y, M, N, d, "Y")
-    _call("svdq_linear_i8", d, stream, _vec(Xq, torch.int8, M * K, d, "Xq"), _vec(sx, torch.float32, M, d, "sx"),
+    _linear_i8(d, stream, _vec(Xq, torch.int8, M * K, d, "Xq"), _vec(sx, torch.float32, M, d, "sx"),
           _vec(Wq, torch.int8, N * K, d, "Wq"), _vec(sw, torch.float32, N, d, "sw"),
           _vec(bias, torch.float32, N, d, "bias"), y, yt, ldy, M, N, K)
 
@@ -496,7 +527,7 @@ def svdq_forward_i8(X, M: int, K: int, inv_s, Wq, sw, bias, Y, N: int, workspace
     d = _cuda_index(X, "X")
     x, xt, ldx = _rows(X, M, K, d, "X")
     y, yt, ldy = _rows(Y, M, N, d, "Y")
-    _call("svdq_forward_i8", d, stream, x, xt, ldx, _vec(inv_s, torch.float32, K, d, "inv_s"),
+    _forward_i8(d, stream, x, xt, ldx, _vec(inv_s, torch.float32, K, d, "inv_s"),
           _vec(Wq, torch.int8, N * K, d, "Wq"), _vec(sw, torch.float32, N, d, "sw"),
           _vec(bias, torch.float32, N, d, "bias"), y, yt, ldy, M, N, K, _vec(workspace, torch.uint8, 0, d, "workspace"),
           0 if workspace is None else workspace.numel())
@@ -519,7 +550,7 @@ def svdq_group_norm(X, B: int, S: int, C: int, G: int, gamma, beta, eps: float, 
     y, yt, ldy = _rows(Y, B * S, C, d, "Y")
     if yt != xt:
         raise TypeError(f"Y: expected dtype {X.dtype}, got {Y.dtype}")
-    _call("svdq_group_norm", d, stream, x, xt, ldx, B, S, C, G, _vec(gamma, torch.float32, C, d, "gamma"),
+    _group_norm(d, stream, x, xt, ldx, B, S, C, G, _vec(gamma, torch.float32, C, d, "gamma"),
           _vec(beta, torch.float32, C, d, "beta"), eps, act, y, ldy, _vec(workspace, torch.uint8, 0, d, "workspace"),
           0 if workspace is None else workspace.numel())
 
@@ -528,7 +559,7 @@ def svdq_group_norm_quantize_i8(X, B: int, S: int, C: int, G: int, gamma, beta, 
                                 workspace, stream=None) -> None:
     d = _cuda_index(X, "X")
     x, xt, ldx = _rows(X, B * S, C, d, "X")
-    _call("svdq_group_norm_quantize_i8", d, stream, x, xt, ldx, B, S, C, G, _vec(gamma, torch.float32, C, d, "gamma"),
+    _group_norm_quantize_i8(d, stream, x, xt, ldx, B, S, C, G, _vec(gamma, torch.float32, C, d, "gamma"),
           _vec(beta, torch.float32, C, d, "beta"), eps, act, _vec(inv_s, torch.float32, C, d, "inv_s"),
           _vec(Xq, torch.int8, B * S * C, d, "Xq"), _vec(sx, torch.float32, B * S, d, "sx"),
           _vec(workspace, torch.uint8, 0, d, "workspace"), 0 if workspace is None else workspace.numel())
