@@ -231,20 +231,17 @@ SVDQ_DEV float rcp(float x) {
   return y;
 }
 SVDQ_DEV float2 silu_f32x2(float2 y) {
-  const float2 d = add_f32x2(make_float2(ex2(-1.44269504f * fmaxf(y.x, -40.0f)), ex2(-1.44269504f * fmaxf(y.y, -40.0f))),
-                             f2(1.0f));
+  const float2 z = mul_f32x2(f2(-1.44269504f), make_float2(fmaxf(y.x, -40.0f), fmaxf(y.y, -40.0f)));
+  const float2 d = add_f32x2(make_float2(ex2(z.x), ex2(z.y)), f2(1.0f));
   const float r = rcp(d.x * d.y);
   return mul_f32x2(y, mul_f32x2(f2(r), make_float2(d.y, d.x)));
 }
 
-SVDQ_DEV void gn_act(float (&y)[8], int act) {
-  if (act == ACT_NONE) return;
-#pragma unroll
-  for (int i = 0; i < 8; i += 2) {
-    const float2 v = make_float2(y[i], y[i + 1]), g = act == ACT_SILU ? silu_f32x2(v) : gelu_f32x2(v);
-    y[i] = g.x;
-    y[i + 1] = g.y;
-  }
+template <int ACT>
+SVDQ_DEV float2 gn_act(float2 y) {
+  if constexpr (ACT == ACT_SILU) return silu_f32x2(y);
+  else if constexpr (ACT == ACT_GELU) return gelu_f32x2(y);
+  else return y;
 }
 
 // A thread's part of the second pass, set up before the statistics are there: its place (l2 threads a row), the
@@ -268,8 +265,10 @@ struct GnApply {
       if constexpr (QUANT) gn_params<VEC>(a.inv_s, 1.0f, c, a.C, is);
     }
   }
-  SVDQ_DEV void fetch(const GroupNormArgs& a, const T* X, const uint4* kept, int lo, int r0, uint32_t (&x)[U][W]) {
+  // Rows r0 - slot, r0 - slot - rp2, ... down to lo; at: the first of them in X.
+  SVDQ_DEV void fetch(const GroupNormArgs& a, const T* at, const uint4* kept, int lo, int r0, uint32_t (&x)[U][W]) {
     if (!on) return;
+    const int64_t step = a.rp2 * a.ldx;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int r = r0 - u * a.rp2 - slot;
@@ -285,7 +284,7 @@ struct GnApply {
           x[u][4 * i + 3] = d.w;
         }
       } else {
-        gn_load<T, VEC>(X + (int64_t)r * a.ldx, c, a.C, x[u]);
+        gn_load<T, VEC>(at - u * step, c, a.C, x[u]);
       }
     }
   }
@@ -294,66 +293,59 @@ struct GnApply {
 // Second pass over rows lo..hi of sample b, from the last to the first (t.fetch has the first step's rows).  stat:
 // (mean, rstd) of the groups; KEEP: the rows are in `kept`.  QUANT: instead of Y, rows of 8-bit codes and their
 // scales.  A row's l2 threads are whole warps, or 4 to 32 lanes of one, a power of two: its maximum is a reduction over lanes, and
-// over warps through `top` (two buffers of U words a warp; one barrier a step).
-template <typename T, bool VEC, bool QUANT, bool KEEP>
-SVDQ_DEV void gn_apply_rows(const GroupNormArgs& a, GnApply<T, VEC, QUANT, KEEP>& t, const T* X, int b, int lo, int hi,
-                            const float2* stat, const uint4* kept, uint32_t* top) {
+// over warps through `top` (two buffers of U words a warp; one barrier of the row's warps a step: l2 >= 64 there, so at
+// most 8 rows and barriers).
+template <typename T, bool VEC, bool QUANT, bool KEEP, int ACT>
+SVDQ_DEV void gn_apply_loop(const GroupNormArgs& a, GnApply<T, VEC, QUANT, KEEP>& t, const T* X, int b, int lo, int hi,
+                            const float2 (&mu)[4], const float2 (&ga)[4], const float2 (&be)[4], const uint4* kept,
+                            uint32_t* top) {
   constexpr int W = Elem<T>::kWords, U = GN_UNROLL<T, QUANT>;
-  const int slot = t.slot, v = t.v, c = t.c, cg = a.C / a.G, lane = threadIdx.x & 31;
+  const int slot = t.slot, v = t.v, c = t.c, lane = threadIdx.x & 31;
   const bool on = t.on;
-  float mu[8];
-  if (on) {
-    int g = c / cg, left = cg * (g + 1) - c;             // the vector's channels, group by group
-    float2 st = stat[g];
+  const auto value = [&](const uint32_t(&w)[W], float2(&y)[4]) {
+    float f[8];
+    Elem<T>::unpack(w, f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (left == 0 && c + i < a.C) {
-        st = stat[++g];
-        left = cg;
-      }
-      --left;
-      mu[i] = st.x;
-      t.ga[i] *= st.y;
-    }
-  }
-  T* Y = static_cast<T*>(a.Y) + (QUANT ? 0 : (int64_t)b * a.S * a.ldy);
-  const auto value = [&](const uint32_t(&w)[W], float(&y)[8]) {
-    Elem<T>::unpack(w, y);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = fmaf(y[i] - mu[i], t.ga[i], t.be[i]);
-    gn_act(y, a.act);
+    for (int i = 0; i < 4; ++i)
+      y[i] = gn_act<ACT>(fma_f32x2(sub_f32x2(make_float2(f[2 * i], f[2 * i + 1]), mu[i]), ga[i], be[i]));
   };
+  const int64_t istep = a.rp2 * a.ldx, ostep = a.rp2 * a.ldy;
+  const T* in = X + (hi - 1 - slot) * a.ldx;
+  T* out = QUANT ? nullptr : static_cast<T*>(a.Y) + ((int64_t)b * a.S + hi - 1 - slot) * a.ldy + c;
   const int nw = a.l2 >> 5;                              // warps a row, 0: part of one
   int buf = 0;
   for (int r0 = hi - 1; r0 >= lo; r0 -= U * a.rp2) {     // uniform over the block
-    if (!KEEP) t.fetch(a, X, kept, lo, r0 - U * a.rp2, t.nx);
+    in -= U * istep;
+    if (!KEEP) t.fetch(a, in, kept, lo, r0 - U * a.rp2, t.nx);
     if constexpr (!QUANT) {
       if (on) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int r = r0 - u * a.rp2 - slot;
           if (r < lo) continue;
-          float y[8];
+          float2 y[4];
           value(t.x[u], y);
-          T* out = Y + (int64_t)r * a.ldy + c;
+          const float f[8] = {y[0].x, y[0].y, y[1].x, y[1].y, y[2].x, y[2].y, y[3].x, y[3].y};
+          T* p = out - u * ostep;
           if constexpr (VEC) {
             uint32_t o[W];
-            Elem<T>::pack(y, o);
+            Elem<T>::pack(f, o);
 #pragma unroll
             for (int i = 0; i < W / 4; ++i) {
               const uint4 d = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-              if (a.streaming) __stcs(reinterpret_cast<uint4*>(out) + i, d);
-              else reinterpret_cast<uint4*>(out)[i] = d;
+              if (a.streaming) __stcs(reinterpret_cast<uint4*>(p) + i, d);
+              else reinterpret_cast<uint4*>(p)[i] = d;
             }
           } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              if (c + i < a.C) out[i] = Elem<T>::from_f32(y[i]);
+              if (c + i < a.C) p[i] = Elem<T>::from_f32(f[i]);
           }
         }
       }
+      out -= U * ostep;
     } else {
-      float y[U][8];
+      float2 y[U][4];
       uint32_t m[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -361,9 +353,9 @@ SVDQ_DEV void gn_apply_rows(const GroupNormArgs& a, GnApply<T, VEC, QUANT, KEEP>
         if (on && r0 - u * a.rp2 - slot >= lo) {
           value(t.x[u], y[u]);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            y[u][i] = __fmul_rn(y[u][i], t.is[i]);
-            m[u] = umax(m[u], abs_bits(y[u][i]));        // C % 16 == 0: whole vectors
+          for (int i = 0; i < 4; ++i) {
+            y[u][i] = mul_f32x2(y[u][i], make_float2(t.is[2 * i], t.is[2 * i + 1]));
+            m[u] = umax(m[u], umax(abs_bits(y[u][i].x), abs_bits(y[u][i].y)));   // C % 16 == 0: whole vectors
           }
         }
       }
@@ -382,8 +374,10 @@ SVDQ_DEV void gn_apply_rows(const GroupNormArgs& a, GnApply<T, VEC, QUANT, KEEP>
 #pragma unroll
         for (int u = 0; u < U; ++u)
           if (lane == u) now[u * (blockDim.x >> 5) + warp] = m[u];
-        __syncthreads();
+        // Only the warps of this row wait for one another, so that the rows' chains of latencies overlap (a row's threads
+        // are whole warps; warps past the last row take no part).
         if (slot < a.rp2) {
+          asm volatile("bar.sync %0, %1;" ::"r"(1 + slot), "r"(a.l2) : "memory");
 #pragma unroll
           for (int u = 0; u < U; ++u)
             for (int k = 0; k < nw; ++k) m[u] = umax(m[u], now[u * (blockDim.x >> 5) + slot * nw + k]);
@@ -401,16 +395,15 @@ SVDQ_DEV void gn_apply_rows(const GroupNormArgs& a, GnApply<T, VEC, QUANT, KEEP>
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int r = r0 - u * a.rp2 - slot;
-        const float mu = __shfl_sync(0xFFFFFFFFu, mul, u, group);
+        const float mul_u = __shfl_sync(0xFFFFFFFFu, mul, u, group);
         if (on && r >= lo) {
-          const float one[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
-          const uint2 code = i8_codes(y[u], one, mu);
-          *reinterpret_cast<uint2*>(a.Xq + ((int64_t)b * a.S + r) * a.C + c) = mu == 0.0f ? make_uint2(0u, 0u) : code;
+          const uint2 code = i8_codes(y[u], mul_u);
+          *reinterpret_cast<uint2*>(a.Xq + ((int64_t)b * a.S + r) * a.C + c) = mul_u == 0.0f ? make_uint2(0u, 0u) : code;
         }
       }
     }
     if (KEEP) {
-      t.fetch(a, X, kept, lo, r0 - U * a.rp2, t.x);
+      t.fetch(a, nullptr, kept, lo, r0 - U * a.rp2, t.x);
     } else {
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -418,6 +411,35 @@ SVDQ_DEV void gn_apply_rows(const GroupNormArgs& a, GnApply<T, VEC, QUANT, KEEP>
         for (int i = 0; i < W; ++i) t.x[u][i] = t.nx[u][i];
     }
   }
+}
+
+template <typename T, bool VEC, bool QUANT, bool KEEP>
+SVDQ_DEV void gn_apply_rows(const GroupNormArgs& a, GnApply<T, VEC, QUANT, KEEP>& t, const T* X, int b, int lo, int hi,
+                            const float2* stat, const uint4* kept, uint32_t* top) {
+  const int c = t.c, cg = a.C / a.G;
+  float2 mu[4], ga[4], be[4];
+  if (t.on) {
+    int g = c / cg, left = cg * (g + 1) - c;             // the vector's channels, group by group
+    float m[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const bool next = left == 0 && c + i < a.C;
+      g += next ? 1 : 0;
+      left = (next ? cg : left) - 1;
+      const float2 st = stat[g];
+      m[i] = st.x;
+      t.ga[i] *= st.y;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      mu[i] = make_float2(m[2 * i], m[2 * i + 1]);
+      ga[i] = make_float2(t.ga[2 * i], t.ga[2 * i + 1]);
+      be[i] = make_float2(t.be[2 * i], t.be[2 * i + 1]);
+    }
+  }
+  if (a.act == ACT_NONE) gn_apply_loop<T, VEC, QUANT, KEEP, ACT_NONE>(a, t, X, b, lo, hi, mu, ga, be, kept, top);
+  else if (a.act == ACT_SILU) gn_apply_loop<T, VEC, QUANT, KEEP, ACT_SILU>(a, t, X, b, lo, hi, mu, ga, be, kept, top);
+  else gn_apply_loop<T, VEC, QUANT, KEEP, ACT_GELU>(a, t, X, b, lo, hi, mu, ga, be, kept, top);
 }
 
 template <typename T, bool VEC>
@@ -445,7 +467,7 @@ __global__ void __launch_bounds__(QUANT ? GN_SMALL_THREADS : GN_MAX_THREADS, 1) 
   const T* X = static_cast<const T*>(a.X) + (int64_t)b * a.S * a.ldx;
   // Inputs may be read before the wait: the first pass started after everything before it was done.
   GnApply<T, VEC, QUANT, false> t(a);
-  t.fetch(a, X, nullptr, lo, hi - 1, t.x);
+  t.fetch(a, X + (hi - 1 - t.slot) * a.ldx, nullptr, lo, hi - 1, t.x);
   griddep_wait();
   griddep_launch_dependents();
   const float2* part = a.part + (int64_t)b * a.P * a.G;

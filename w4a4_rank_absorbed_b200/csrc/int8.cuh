@@ -146,19 +146,26 @@ __global__ void __launch_bounds__(PW8_THREADS) k_pack_weight_i8(const float* __r
   }
 }
 
-// Eight codes of x_hat = x s as one byte each: f32(x_hat mul) plus 1.5 2^23 leaves rint of it (to even, as the
-// sum is rounded to whole numbers) in the low bits of the sum, whose low byte is the code.
-SVDQ_DEV uint2 i8_codes(const float (&x)[8], const float (&s)[8], float mul) {
+// Eight codes of x_hat as one byte each: f32(x_hat mul) plus 1.5 2^23 leaves rint of it (to even, as the sum is
+// rounded to whole numbers) in the low bits of the sum, whose low byte is the code.  (Product and sum not as packed
+// pairs: those came out as one fused operation, off at ties.)
+SVDQ_DEV uint2 i8_codes(const float2 (&xh)[4], float mul) {
   uint32_t c[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 xh = mul_f32x2(make_float2(x[2 * i], x[2 * i + 1]), make_float2(s[2 * i], s[2 * i + 1]));
-    // (not as packed pairs: a packed product and sum came out as one fused operation, off at ties)
-    c[2 * i] = __float_as_uint(__fadd_rn(__fmul_rn(xh.x, mul), 12582912.0f));
-    c[2 * i + 1] = __float_as_uint(__fadd_rn(__fmul_rn(xh.y, mul), 12582912.0f));
+    c[2 * i] = __float_as_uint(__fadd_rn(__fmul_rn(xh[i].x, mul), 12582912.0f));
+    c[2 * i + 1] = __float_as_uint(__fadd_rn(__fmul_rn(xh[i].y, mul), 12582912.0f));
   }
   return make_uint2(__byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410),
                     __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410));
+}
+// The same of x_hat = f32(x s).
+SVDQ_DEV uint2 i8_codes(const float (&x)[8], const float (&s)[8], float mul) {
+  float2 xh[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    xh[i] = mul_f32x2(make_float2(x[2 * i], x[2 * i + 1]), make_float2(s[2 * i], s[2 * i + 1]));
+  return i8_codes(xh, mul);
 }
 
 // Activation quantization.  A group of threads, a warp or a block, owns a row at a time, each thread VPT vectors
