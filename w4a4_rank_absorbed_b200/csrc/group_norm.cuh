@@ -349,15 +349,16 @@ SVDQ_DEV void gn_apply_loop(const GroupNormArgs& a, GnApply<T, VEC, QUANT, KEEP>
       uint32_t m[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        m[u] = 0u;
+        float top_u = 0.0f;
         if (on && r0 - u * a.rp2 - slot >= lo) {
           value(t.x[u], y[u]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             y[u][i] = mul_f32x2(y[u][i], make_float2(t.is[2 * i], t.is[2 * i + 1]));
-            m[u] = umax(m[u], umax(abs_bits(y[u][i].x), abs_bits(y[u][i].y)));   // C % 16 == 0: whole vectors
+            top_u = max_abs(top_u, y[u][i].x, y[u][i].y);            // C % 16 == 0: whole vectors
           }
         }
+        m[u] = __float_as_uint(top_u);
       }
       __syncwarp();                                      // the lanes parted above
       if (nw) {
@@ -384,18 +385,20 @@ SVDQ_DEV void gn_apply_loop(const GroupNormArgs& a, GnApply<T, VEC, QUANT, KEEP>
         }
         buf ^= 1;
       }
-      // lane j of a row's threads works out the scale of its row j of the U (two divisions), for all of them
-      const int group = min(a.l2, 32), j = lane & (group - 1);
+      // Of a row's first 2 U threads, j works out the multiplier of its row j of the U or, from U on, the scale of row
+      // j - U: one division for all.
+      static_assert((U & (U - 1)) == 0 && 2 * U <= 4, "at least 2 U lanes a row");
+      const int group = min(a.l2, 32), j = lane & (group - 1) & (U - 1);
       uint32_t own = m[0];
 #pragma unroll
       for (int u = 1; u < U; ++u) own = j == u ? m[u] : own;
-      float scale, mul;
-      i8_scale(own, scale, mul);
-      if (v < U && slot < a.rp2 && r0 - v * a.rp2 - slot >= lo) a.sx[(int64_t)b * a.S + r0 - v * a.rp2 - slot] = scale;
+      const float either = i8_scale_or_mul(own, (lane & U) != 0);
+      if (v >= U && v < 2 * U && slot < a.rp2 && r0 - j * a.rp2 - slot >= lo)
+        a.sx[(int64_t)b * a.S + r0 - j * a.rp2 - slot] = either;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int r = r0 - u * a.rp2 - slot;
-        const float mul_u = __shfl_sync(0xFFFFFFFFu, mul, u, group);
+        const float mul_u = __shfl_sync(0xFFFFFFFFu, either, u, group);
         if (on && r >= lo) {
           const uint2 code = i8_codes(y[u], mul_u);
           *reinterpret_cast<uint2*>(a.Xq + ((int64_t)b * a.S + r) * a.C + c) = mul_u == 0.0f ? make_uint2(0u, 0u) : code;

@@ -89,6 +89,12 @@ SVDQ_DEV void load8(const T* p, uint32_t (&w)[Elem<T>::kWords]) {
 // |x| as an unsigned integer: the order of magnitudes, with infinities and NaN above every number.
 SVDQ_DEV uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 SVDQ_DEV uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+// max(m, |a|, |b|) for m >= 0; NaN (as 0x7FFFFFFF) if any is.  Its bits order as abs_bits' do.
+SVDQ_DEV float max_abs(float m, float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
+}
 
 // Scale and multiplier of a row (or channel) whose largest magnitude has the bits `a`.
 SVDQ_DEV void i8_scale(uint32_t a, float& scale, float& mul) {
@@ -102,6 +108,13 @@ SVDQ_DEV void i8_scale(uint32_t a, float& scale, float& mul) {
     scale = __fdiv_rn(__uint_as_float(a), 127.0f);
     mul = __fdiv_rn(127.0f, __uint_as_float(a));
   }
+}
+// One of the two, by one division: lanes that need either then exchange them.
+SVDQ_DEV float i8_scale_or_mul(uint32_t a, bool scale) {
+  if (a >= 0x7F800000u) return scale ? __uint_as_float(0x7FC00000u) : 0.0f;
+  if (a < ((127u - 100u) << 23)) return 0.0f;
+  const float top = __uint_as_float(a);
+  return __fdiv_rn(scale ? top : 127.0f, scale ? 127.0f : top);
 }
 // Code of x (0 whatever x is where mul = 0: an infinite x times 0 is NaN, which has no integer).
 SVDQ_DEV int i8_code(float x, float mul) { return mul == 0.0f ? 0 : __float2int_rn(__fmul_rn(x, mul)); }
@@ -223,7 +236,7 @@ __global__ void __launch_bounds__(WARP ? 256 : QI_MAX_THREADS) k_quantize_act_i8
   fetch(row, w);
   for (; row < M; row += step) {                         // uniform over the group
     fetch(row + step, nx);
-    uint32_t a = 0u;
+    float top = 0.0f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       float f[8];
@@ -231,19 +244,19 @@ __global__ void __launch_bounds__(WARP ? 256 : QI_MAX_THREADS) k_quantize_act_i8
 #pragma unroll
       for (int i = 0; i < 8; i += 2) {
         const float2 h = mul_f32x2(make_float2(f[i], f[i + 1]), make_float2(s[j][i], s[j][i + 1]));
-        a = umax(a, umax(abs_bits(h.x), abs_bits(h.y)));
+        top = max_abs(top, h.x, h.y);
       }
     }
-    a = __reduce_max_sync(0xFFFFFFFFu, a);
+    uint32_t a = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top));
     if (!WARP) {
       if (lane == 0) part[buf][warp] = a;                // two buffers: one barrier a row
       __syncthreads();
       a = __reduce_max_sync(0xFFFFFFFFu, lane < (size >> 5) ? part[buf][lane] : 0u);
       buf ^= 1;
     }
-    float scale, mul;
-    i8_scale(a, scale, mul);
-    if (me == 0) sx[row] = scale;
+    const float either = i8_scale_or_mul(a, lane == 0);  // lane 0 the scale, the others the multiplier
+    if (me == 0) sx[row] = either;
+    const float mul = __shfl_sync(0xFFFFFFFFu, either, 1);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int v = me + j * size;
