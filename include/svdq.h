@@ -354,7 +354,7 @@ SVDQ_API svdq_status svdq_gelu_bf16(const uint16_t* X, int64_t n, uint16_t* Y, s
  *   - a infinite or NaN: scale NaN and all codes 0 (the output row is NaN).
  * Element types are given by svdq_dtype.  Shapes: K % 16 == 0, K < 131072 (the
  * 32-bit sum cannot overflow below that), N >= 1, M >= 0 (M = 0 launches nothing;
- * its buffer pointers may be NULL).  Row pitches (ldx, ldy) count elements; a
+ * its buffer pointers may be NULL), M and N at most 2^31 - 1024.  Row pitches (ldx, ldy) count elements; a
  * row of X starts on 16 bytes (ldx times the element size % 16 == 0), a row of Y
  * anywhere (ldy >= N).  Pointers are 16-byte aligned as for every call.
  */
@@ -418,12 +418,16 @@ SVDQ_API svdq_status svdq_forward_i8(const void* X, int x_type, int64_t ldx, con
  *               (sample b starts at row b S).
  *   gamma, beta [in] float32, C, or NULL (1 and 0).
  *   eps >= 0, act an svdq_act.
- *   Y     [out] type, rows at pitch ldy (channels past C are not touched); Y may be X.
- *   workspace [in/out] svdq_group_norm_workspace_bytes(B, S, C, G) bytes; zero it
- *               once after allocating it (and again after a call that reported
- *               SVDQ_ERR_TIMEOUT); calls that may overlap need their own.
- * Shapes: C % G == 0, C <= 4096; any S and B (0 launches nothing), any pitch >= C.
- * Values whose squared deviation leaves float32's range give a non-finite result.
+ *   Y     [out] type, rows at pitch ldy (channels past C are not touched).  Y may be
+ *               X itself (ldy = ldx); it must not overlap X in any other way.
+ *   workspace [scratch] svdq_group_norm_workspace_bytes(B, S, C, G) bytes (16 at
+ *               least), no initial contents needed; calls that may overlap need
+ *               workspaces of their own.
+ * Shapes: C % G == 0, C <= 4096, S <= 2^30, B S < 2^31 (B or S = 0 launches nothing),
+ * any pitch >= C.  Rows that start on 16 bytes with C % 8 == 0 take vector loads.
+ * Where a cluster of eight blocks holds a sample, one launch that reads X once;
+ * else two launches.  Values whose squared deviation leaves float32's range give a
+ * non-finite result; an infinite or NaN value makes its group's results NaN.
  */
 typedef enum {
     SVDQ_ACT_NONE = 0,

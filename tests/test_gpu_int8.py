@@ -66,7 +66,7 @@ def _linear(C, xq, sx, wq, sw, bias, kind, pad=0):
 SHAPES = [(1, 16, 16), (1, 1, 16), (2, 17, 32), (1, 4096, 4096), (3, 130, 144), (15, 257, 272), (16, 128, 128),
           (17, 127, 400), (31, 1000, 1040), (33, 640, 1296), (64, 256, 512), (65, 255, 528), (77, 1288, 2048),
           (127, 129, 256), (128, 384, 1024), (129, 100, 112), (200, 3, 2064), (255, 512, 640), (257, 513, 656),
-          (300, 1024, 12288), (513, 768, 128), (1000, 1001, 1040), (1024, 2048, 512), (2049, 300, 272), (4608, 33, 64)]
+          (300, 1024, 12288), (513, 768, 128), (1000, 1001, 1040), (1024, 2048, 512), (2049, 300, 272), (4608, 33, 64), (700, 160, 256), (2304, 320, 320), (5000, 224, 128), (9500, 480, 96)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)

@@ -36,7 +36,7 @@ NORMQ = dict(X=16, type=0, ldx=64, B=2, S=3, C=64, G=4, gamma=16, beta=16, eps=1
 @pytest.mark.parametrize("name,base,cases", [
     ("svdq_linear_i8", LINEAR, [
         (dict(K=72), UNSUP), (dict(K=1 << 17), UNSUP), (dict(K=0), INVAL), (dict(N=0), INVAL), (dict(M=-1), INVAL),
-        (dict(M=1 << 31), UNSUP), (dict(N=1 << 31, ldy=1 << 31), UNSUP), (dict(Xq=None), INVAL), (dict(sx=None), INVAL),
+        (dict(M=1 << 31), UNSUP), (dict(M=(1 << 31) - 1023), UNSUP), (dict(N=1 << 31, ldy=1 << 31), UNSUP), (dict(Xq=None), INVAL), (dict(sx=None), INVAL),
         (dict(Wq=None), INVAL), (dict(sw=None), INVAL), (dict(Y=None), INVAL), (dict(y_type=3), INVAL),
         (dict(y_type=-1), INVAL), (dict(ldy=95), INVAL), (dict(Xq=8), ALIGN), (dict(Y=24), ALIGN), (dict(bias=8), ALIGN),
         (dict(sw=4), ALIGN), (dict(M=0, Xq=None, sx=None, Y=None), OK), (dict(M=0, K=72), UNSUP),
@@ -51,7 +51,7 @@ NORMQ = dict(X=16, type=0, ldx=64, B=2, S=3, C=64, G=4, gamma=16, beta=16, eps=1
         (dict(ldx=60), INVAL), (dict(ldy=5), INVAL), (dict(M=0, X=None, Y=None, ws=None, wsb=0), OK)]),
     ("svdq_group_norm", NORM, [
         (dict(G=5), UNSUP), (dict(C=4104, ldx=4104, ldy=4104), UNSUP), (dict(G=0), INVAL), (dict(C=0), INVAL),
-        (dict(B=-1), INVAL), (dict(S=-1), INVAL), (dict(B=1 << 16, S=1 << 16), UNSUP), (dict(type=3), INVAL),
+        (dict(B=-1), INVAL), (dict(S=-1), INVAL), (dict(B=1 << 16, S=1 << 16), UNSUP), (dict(B=1, S=(1 << 30) + 1), UNSUP), (dict(type=3), INVAL),
         (dict(act=3), INVAL), (dict(act=-1), INVAL), (dict(eps=-1.0), INVAL), (dict(eps=float("nan")), INVAL),
         (dict(eps=float("inf")), INVAL), (dict(X=None), INVAL), (dict(Y=None), INVAL), (dict(ldx=63), INVAL),
         (dict(ldy=63), INVAL), (dict(X=2), ALIGN), (dict(ws=None), INVAL), (dict(wsb=8), INVAL), (dict(ws=8), ALIGN),

@@ -118,10 +118,6 @@ SVDQ_DEV float i8_scale_or_mul(uint32_t a, bool scale) {
 }
 // Code of x (0 whatever x is where mul = 0: an infinite x times 0 is NaN, which has no integer).
 SVDQ_DEV int i8_code(float x, float mul) { return mul == 0.0f ? 0 : __float2int_rn(__fmul_rn(x, mul)); }
-SVDQ_DEV uint32_t pack_i8x4(int a, int b, int c, int d) {
-  return (uint32_t)(a & 0xFF) | ((uint32_t)(b & 0xFF) << 8) | ((uint32_t)(c & 0xFF) << 16) | ((uint32_t)(d & 0xFF) << 24);
-}
-
 // Weight packing: W_hat (K x N float32, N contiguous) -> Wq (N x K codes), sw (N).  A block takes 32
 // columns: its 16 warps walk the rows once for the column maxima (lane = column, 128-byte rows) and once
 // more for the codes, turned through a shared tile of 128 rows so that Wq is written along K.

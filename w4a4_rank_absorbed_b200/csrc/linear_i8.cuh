@@ -41,13 +41,13 @@ SVDQ_DEV void store_y(void* Y, int type, int64_t at, float y) {
 }
 
 // ------------------------------------------------------------------ pair kernel ---
-// Many tokens: persistent CTA pairs (one CTA an SM), tiles of 256 tokens x nt channels (nt 64..256), each
+// Many tokens: persistent CTA pairs (one CTA an SM), tiles of 256 tokens x nt channels (nt a multiple of 32, 64..256), each
 // CTA holding 128 of the tokens and half of the channels' codes in a 6-slot ring of 32 KB, and the sums of
 // its 128 tokens in TMEM twice over (columns 0 and 256), so that a tile's epilogue runs under the next
 // tile's MMAs.  A pair's MMA reads each operand byte from shared memory half as often as two CTAs' own
 // would, and each CTA copies half of B.
-//   warp 0      copies (one thread): A and B boxes, both CTAs counting on the leader's barrier
-//   warp 1      leader only: MMAs (one thread);  in both: TMEM
+//   warp 0      copies: A and B boxes, both CTAs counting on the leader's barrier
+//   warp 1      leader only: MMAs;  in both: TMEM
 //   warps 4-11  epilogue: TMEM -> registers, scales and bias, stores (two warps a lane quarter)
 constexpr int LP_STAGES = 6;
 constexpr int LP_A_BYTES = 128 * 128;
@@ -266,17 +266,17 @@ __global__ void __launch_bounds__(LP_THREADS, 1) k_linear_i8_pair(
     const int ew = warp - LP_EPI_WARP0, q = warp & 3, h = ew >> 2;
     float* stg = reinterpret_cast<float*>(smem + LP_OFF_STG + ew * LP_STG_BYTES);
     float* chan = stg + 512;
-    const int chunks = a.nt >> 6;                        // 32-column chunks of this warp's half of the tile
+    const int last = (((a.nt >> 5) - 1 - h) & ~1) + h;   // this warp's 32-column chunks: h, h + 2, .. last
     int n = 0;
     for (int t = first; t < total; t += step, ++n) {
       int mb, nb;
       pair_tile(t, num_m, num_n, mb, nb);
-      const int row0 = mb * 256 + (int)rank * 128 + 32 * q, col0 = nb * a.nt + h * (a.nt >> 1);
+      const int row0 = mb * 256 + (int)rank * 128 + 32 * q, col0 = nb * a.nt + 32 * h;
       const float sx = row0 + lane < a.M ? __ldg(a.sx + row0 + lane) : 0.0f;
       __syncwarp();                                      // the last tile's reads of them are done
       // the tile's channel scales and biases, while the sums are on their way
-      if (4 * lane < (a.nt >> 1)) {
-        const int c = col0 + 4 * lane;
+      if (h + 2 * (lane >> 3) <= last) {                 // four columns a lane
+        const int c = col0 + 64 * (lane >> 3) + 4 * (lane & 7);
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f), b = s;
         if (c + 4 <= a.N) {
           s = __ldg(reinterpret_cast<const float4*>(a.sw + c));
@@ -297,18 +297,18 @@ __global__ void __launch_bounds__(LP_THREADS, 1) k_linear_i8_pair(
       __syncwarp();
       if (!__all_sync(0xFFFFFFFFu, mbar_wait(&acc_full[n & 1], (uint32_t)((n >> 1) & 1), tmo, abort_flag, 0x521))) break;
       tc_fence_after();
-      const uint32_t ta = tbase + 256u * (uint32_t)(n & 1) + ((uint32_t)(32 * q) << 16) + (uint32_t)(h * (a.nt >> 1));
-      for (int c = 0; c < chunks; ++c) {
+      const uint32_t ta = tbase + 256u * (uint32_t)(n & 1) + ((uint32_t)(32 * q) << 16);
+      for (int c = h; c <= last; c += 2) {
         uint32_t v[32];
         tmem_ld_32x32b_x32(ta + 32 * c, v);
         tmem_ld_wait();
         reg_fence(v);
-        if (c == chunks - 1) {                           // all of this tile's sums are in registers: release it
+        if (c == last) {                                 // all of this tile's sums are in registers: release it
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&acc_empty[n & 1]), 0));
         }
-        store_chunk(a, v, row0, col0 + 32 * c, sx, smem_u32(chan) + 128u * (uint32_t)c, stg);
+        store_chunk(a, v, row0, nb * a.nt + 32 * c, sx, smem_u32(chan) + 64u * (uint32_t)(c - h), stg);
       }
     }
   }
@@ -327,7 +327,10 @@ __global__ void __launch_bounds__(LP_THREADS, 1) k_linear_i8_pair(
 // full whatever N is.  Each CTA streams its K range through a ring, leaves its integer sums in shared
 // memory, and after a cluster barrier sums a share of the tile's outputs over the cluster's CTAs (integers:
 // the order does not matter).
-//   warp 0  copies, warp 1 MMAs and TMEM (one thread each);  then all eight warps the epilogue
+//   warp 0  copies, warp 1 MMAs and TMEM;  then all eight warps the epilogue
+// TMEM: CTAs of several such kernels may share an SM, and one that waits for columns while its cluster waits for it
+// must not meet another in the same position.  With a cluster a CTA has at least two ring slots, so at most six (nt
+// 16..32: 32 columns each), four (33..80: 64 or 128) or three (81..128: 128) fit an SM's shared memory: 512 columns always do.
 constexpr int LS_THREADS = 256;
 constexpr int LS_A_BYTES = 128 * 128;
 constexpr int LS_TAIL_BYTES = 256 + 1024;                 // barriers, then the tile's token scales

@@ -448,13 +448,20 @@ svdq_status linear_impl(const uint8_t* Xq, const uint8_t* SFx, float gs_x, const
 
 // ------------------------------------------------------------- int8 layer ---
 constexpr int64_t kMaxK8 = int64_t(1) << 17;      // 128 * 128 * K stays inside the 32-bit sum below this
+constexpr int64_t kMaxRows8 = (int64_t(1) << 31) - 1024;   // rows and columns, rounded up to tiles, stay in 32 bits
+
+// A call that failed to launch: its error must not be taken for a later call's.
+svdq_status launch_failed() {
+  (void)cudaGetLastError();
+  return SVDQ_ERR_CUDA;
+}
 
 size_t dtype_size(int type) { return type == SVDQ_FP32 ? 4 : 2; }
 bool dtype_ok(int type) { return type == SVDQ_BF16 || type == SVDQ_FP32 || type == SVDQ_FP16; }
 
 svdq_status check_shape_i8(int64_t M, int64_t N, int64_t K) {
   if (M < 0 || N < 1 || K < 1) return SVDQ_ERR_INVALID_ARG;
-  if (M > kMaxDim || N > kMaxDim || K >= kMaxK8 || K % 16 != 0) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+  if (M > kMaxRows8 || N > kMaxRows8 || K >= kMaxK8 || K % 16 != 0) return SVDQ_ERR_UNSUPPORTED_SHAPE;
   return SVDQ_OK;
 }
 
@@ -498,7 +505,7 @@ svdq_status quantize_i8(DevInfo* d, const void* Xv, int64_t ldx, int64_t M, int6
       : nv <= 2048         ? run_quantize_i8<T, 4, false>(d, X, M, K, ldx, inv_s, Xq, sx, s)
                            : launch_pdl(k_quantize_long_i8<T>, dim3((unsigned)M), dim3(QI_MAX_THREADS), 0, s, 1, X,
                                         (int)K, ldx, inv_s, Xq, sx);
-  return e == cudaSuccess ? launch_status() : SVDQ_ERR_CUDA;
+  return e == cudaSuccess ? launch_status() : launch_failed();
 }
 svdq_status launch_quantize_i8(DevInfo* d, const void* X, int x_type, int64_t ldx, int64_t M, int64_t K,
                                const float* inv_s, int8_t* Xq, float* sx, cudaStream_t s) {
@@ -512,7 +519,7 @@ template <typename F>
 svdq_status allow_smem(F kernel, int dev, std::atomic<bool> (&done)[kMaxDevices], int bytes) {
   if (done[dev].load(std::memory_order_acquire)) return SVDQ_OK;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
-    return SVDQ_ERR_CUDA;
+    return launch_failed();
   done[dev].store(true, std::memory_order_release);
   return SVDQ_OK;
 }
@@ -543,7 +550,7 @@ LinearI8Plan find_plan_linear_i8(int64_t M, int64_t N, int64_t K, int sms) {
   LinearI8Plan best = {true, 256, 1};
   double least = 1e30;
   const auto waves = [](int64_t tiles, int64_t at_once) { return (double)((tiles + at_once - 1) / at_once); };
-  for (int nt = 256; nt >= 64; nt -= 64) {
+  for (int nt = 256; nt >= 64; nt -= 32) {
     const int64_t tiles = (M + 255) / 256 * ((N + nt - 1) / nt);
     const double main = (double)nkt * (0.11 + 0.001 * nt);
     const double t = 2.6 + main + (waves(tiles, sms / 2) - 1) * std::max(main, 1.65 + 0.0068 * nt) + 0.3 + 0.0095 * nt;
@@ -622,7 +629,7 @@ svdq_status launch_linear_i8(int dev, DevInfo* d, const int8_t* Xq, const float*
     if ((st = allow_smem(k_linear_i8_pair, dev, g_pair_attr, LP_SMEM)) != SVDQ_OK) return st;
     if (launch_pdl(k_linear_i8_pair, dim3((unsigned)(2 * std::min<int64_t>(tiles, d->sms / 2))), dim3(LP_THREADS),
                    (size_t)LP_SMEM, s, 2, tm_x, tm_w, a) != cudaSuccess)
-      return SVDQ_ERR_CUDA;
+      return launch_failed();
     return launch_status();
   }
   // A ring of at most 100 KB: two CTAs fit an SM, so that the next kernel's start overlaps this one's end.
@@ -633,12 +640,13 @@ svdq_status launch_linear_i8(int dev, DevInfo* d, const int8_t* Xq, const float*
   if ((st = allow_smem(k_linear_i8_split, dev, g_split_attr, 100 * 1024 + LS_TAIL_BYTES + 1024)) != SVDQ_OK) return st;
   if (launch_pdl(k_linear_i8_split, dim3((unsigned)((N + 127) / 128 * p.split), (unsigned)((M + p.nt - 1) / p.nt)),
                  dim3(LS_THREADS), smem, s, p.split, tm_w, tm_x, a, p.split) != cudaSuccess)
-    return SVDQ_ERR_CUDA;
+    return launch_failed();
   return launch_status();
 }
 
 // ------------------------------------------------------------- group norm ---
 constexpr int64_t kMaxNormC = GN_MAX_C;
+constexpr int64_t kMaxNormS = int64_t(1) << 30;   // row numbers a few blocks past the end stay in 32 bits
 
 constexpr int64_t kNormBlocks = 148;      // one block an SM of a B200
 constexpr int kNormSmem = 232448 - 2048;  // dynamic shared memory of k_group_norm, at most
@@ -746,14 +754,14 @@ svdq_status launch_norm(int dev, const NormArgs& n, cudaStream_t s) {
     if (st != SVDQ_OK) return st;
     const size_t smem = (size_t)gn_fixed_floats(a.G, p.threads1) * 4 + (size_t)p.rows * (size_t)row_bytes;
     if (launch_pdl(k_group_norm<T, VEC, QUANT>, dim3((unsigned)blocks), dim3(p.threads1), smem, s, p.P, a) != cudaSuccess)
-      return SVDQ_ERR_CUDA;
+      return launch_failed();
     return launch_status();
   }
   if (launch_pdl(k_group_stats<T, VEC>, dim3((unsigned)blocks), dim3(p.threads1), 0, s, 1, a) != cudaSuccess)
-    return SVDQ_ERR_CUDA;
+    return launch_failed();
   const size_t smem = ((size_t)n.G + 1) / 2 * 2 * sizeof(float2) + (size_t)p.threads2 * sizeof(GnMerge);
   if (launch_pdl(k_group_apply<T, VEC, QUANT>, dim3((unsigned)blocks), dim3(p.threads2), smem, s, 1, a) != cudaSuccess)
-    return SVDQ_ERR_CUDA;
+    return launch_failed();
   return launch_status();
 }
 template <typename T, bool QUANT>
@@ -767,7 +775,7 @@ svdq_status norm_impl(const NormArgs& n, cudaStream_t s) {
   if (n.B < 0 || n.S < 0 || n.C < 1 || n.G < 1 || !dtype_ok(n.type) || n.act < SVDQ_ACT_NONE ||
       n.act > SVDQ_ACT_GELU || !(n.eps >= 0.0f) || !std::isfinite(n.eps))
     return SVDQ_ERR_INVALID_ARG;
-  if (n.C % n.G != 0 || n.C > kMaxNormC || (QUANT && n.C % 16 != 0) || n.B > kMaxDim || n.S > kMaxDim ||
+  if (n.C % n.G != 0 || n.C > kMaxNormC || (QUANT && n.C % 16 != 0) || n.B > kMaxDim || n.S > kMaxNormS ||
       (n.B > 0 && n.S > kMaxDim / n.B))
     return SVDQ_ERR_UNSUPPORTED_SHAPE;
   if (n.B == 0 || n.S == 0) return SVDQ_OK;        // an empty batch: nothing to launch
@@ -1018,7 +1026,7 @@ svdq_status svdq_forward_i8(const void* X, int x_type, int64_t ldx, const float*
 }
 
 size_t svdq_group_norm_workspace_bytes(int64_t B, int64_t S, int64_t C, int64_t G) {
-  if (B < 1 || S < 1 || C < 1 || G < 1 || C % G != 0 || C > kMaxNormC || B > kMaxDim || S > kMaxDim / B)
+  if (B < 1 || S < 1 || C < 1 || G < 1 || C % G != 0 || C > kMaxNormC || B > kMaxDim || S > kMaxNormS || S > kMaxDim / B)
     return 0;
   return group_norm_workspace(B, S, C, G);
 }

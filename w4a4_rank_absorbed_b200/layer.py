@@ -296,7 +296,6 @@ class GroupNorm:
         self.device, self.G, self.C, self.eps, self.act = dev, num_groups, num_channels, float(eps), self._ACTS[act]
         self.weight = None if weight is None else weight.to(dev, torch.float32).contiguous()
         self.bias = None if bias is None else bias.to(dev, torch.float32).contiguous()
-        self._ws: Dict[tuple, torch.Tensor] = {}
 
     def _rows(self, X: torch.Tensor):
         if X.dim() < 2 or X.shape[-1] != self.C:
@@ -309,17 +308,8 @@ class GroupNorm:
         return B, S
 
     def _workspace(self, B: int, S: int):
-        """One workspace per stream and shape.  A call that is being captured gets one of its own, zeroed
-        inside the graph: graphs replayed at the same time share none."""
-        if B == 0 or S == 0:
-            return None
-        if torch.cuda.is_current_stream_capturing():
-            return _C.new_group_norm_workspace(B, S, self.C, self.G, self.device)
-        key = (torch.cuda.current_stream(self.device).cuda_stream, B, S)
-        ws = self._ws.get(key)
-        if ws is None:
-            ws = self._ws[key] = _C.new_group_norm_workspace(B, S, self.C, self.G, self.device)
-        return ws
+        """From torch's allocator on the current stream: calls on several streams and captured graphs share none."""
+        return _C.new_group_norm_workspace(B, S, self.C, self.G, self.device)
 
     def forward(self, X: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         B, S = self._rows(X)

@@ -538,9 +538,10 @@ def svdq_group_norm_workspace_bytes(B: int, S: int, C: int, G: int) -> int:
 
 
 def new_group_norm_workspace(B: int, S: int, C: int, G: int, device=None) -> Optional[torch.Tensor]:
-    """A zero-filled workspace for the group norms of this shape (None for a shape they refuse)."""
+    """A workspace for the group norms of this shape (None for an empty batch or a shape they refuse); its contents need
+    no initial value."""
     n = svdq_group_norm_workspace_bytes(B, S, C, G)
-    return torch.zeros(n, dtype=torch.uint8, device=device if device is not None else "cuda") if n else None
+    return torch.empty(n, dtype=torch.uint8, device=device if device is not None else "cuda") if n else None
 
 
 def svdq_group_norm(X, B: int, S: int, C: int, G: int, gamma, beta, eps: float, act: int, Y, workspace,
