@@ -95,6 +95,14 @@ def test_group_norm(B, S, C, G, kind):
     _check(Y, X, G, gamma, beta, 1e-5, act, kind)
 
 
+@pytest.mark.parametrize("B,S,C,G,kind", [(1, 300000, 128, 32, "bf16"), (3, 70001, 96, 8, "fp32"), (2, 90000, 200, 40, "fp16")])
+def test_tensors_larger_than_the_cache_share(B, S, C, G, kind):
+    """Above 64 MB the first pass marks the rows that the second is to find in L2, and its blocks are wider."""
+    X, gamma, beta = _case(B, S, C, kind, 77)
+    assert X.numel() * X.element_size() > 64 << 20
+    _check(_run(X, B, S, C, G, gamma, beta, 1e-5, "silu"), X, G, gamma, beta, 1e-5, "silu", kind)
+
+
 @pytest.mark.parametrize("act", ["none", "silu", "gelu"])
 @pytest.mark.parametrize("kind", ["bf16", "fp16", "fp32"])
 def test_activations_without_affine(act, kind):

@@ -51,6 +51,7 @@ struct GroupNormArgs {
   const float* beta;
   float eps;
   int act;
+  int hot;                // rows of a block before those that L2 is to hold until the second pass
   int streaming;          // Y is larger than L2 would keep: stores that do not displace X
   void* Y;
   int64_t ldy;
@@ -98,12 +99,29 @@ SVDQ_DEV void gn_load(const T* p, int c, int C, uint32_t (&w)[Elem<T>::kWords]) 
   }
 }
 
+// The same as vectors, and how L2 ranks the lines that the load brings: those to be read again soon before the rest.
+SVDQ_DEV uint64_t l2_policy(bool again) {
+  uint64_t first, normal;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(first));
+  asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(normal));
+  return again ? normal : first;
+}
+template <typename T>
+SVDQ_DEV void gn_load(const T* p, int c, uint64_t policy, uint32_t (&w)[Elem<T>::kWords]) {
+#pragma unroll
+  for (int i = 0; i < Elem<T>::kWords / 4; ++i)
+    asm volatile("ld.global.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
+                 : "=r"(w[4 * i]), "=r"(w[4 * i + 1]), "=r"(w[4 * i + 2]), "=r"(w[4 * i + 3])
+                 : "l"(reinterpret_cast<const uint4*>(p + c) + i), "l"(policy));
+}
+
 // M2 is never negative but for rounding; a NaN stays one.
 SVDQ_DEV float gn_m2(float v) { return v < 0.0f ? 0.0f : v; }
 
 // First pass over the block's rows lo..hi: (mean, M2) of each group to out (shared or global memory).  sum and
-// sq: 8 floats a thread each.  KEEP: the rows also go to `kept` (row by row, nv vectors).
-template <typename T, bool VEC, bool KEEP>
+// sq: 8 floats a thread each.  KEEP: the rows also go to `kept` (row by row, nv vectors).  LARGE: the tensor is larger
+// than L2; the rows before a.hot are not to displace those after it, which the second pass reads first.
+template <typename T, bool VEC, bool KEEP, bool LARGE>
 SVDQ_DEV void gn_block_stats(const GroupNormArgs& a, const T* X, int lo, int hi, float* sum, float* sq, uint4* kept,
                              float2* out) {
   constexpr int W = Elem<T>::kWords, U = GN_UNROLL<T, false>;
@@ -111,10 +129,16 @@ SVDQ_DEV void gn_block_stats(const GroupNormArgs& a, const T* X, int lo, int hi,
   const int width = 8 * a.nv, cg = a.C / a.G, lane = threadIdx.x & 31;
   if (slot < a.rp1) {
     uint32_t x[U][W], nx[U][W];
+    const uint64_t once = l2_policy(false), again = l2_policy(true);
     const auto fetch = [&](int r0, uint32_t(&x)[U][W]) {
+      const uint64_t policy = r0 >= lo + a.hot ? again : once;
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (r0 + u * a.rp1 < hi) gn_load<T, VEC>(X + (int64_t)(r0 + u * a.rp1) * a.ldx, c, a.C, x[u]);
+      for (int u = 0; u < U; ++u) {
+        if (r0 + u * a.rp1 >= hi) continue;
+        const T* row = X + (int64_t)(r0 + u * a.rp1) * a.ldx;
+        if constexpr (LARGE) gn_load<T>(row, c, policy, x[u]);
+        else gn_load<T, VEC>(row, c, a.C, x[u]);
+      }
     };
     fetch(lo + slot, x);                                 // in flight together with the pivots
     float pivot[8], s[8], q[8];
@@ -445,14 +469,14 @@ SVDQ_DEV void gn_apply_rows(const GroupNormArgs& a, GnApply<T, VEC, QUANT, KEEP>
   else gn_apply_loop<T, VEC, QUANT, KEEP, ACT_GELU>(a, t, X, b, lo, hi, mu, ga, be, kept, top);
 }
 
-template <typename T, bool VEC>
+template <typename T, bool VEC, bool LARGE>
 __global__ void __launch_bounds__(GN_MAX_THREADS, 1) k_group_stats(const GroupNormArgs a) {
   __shared__ __align__(16) float sum[8 * GN_MAX_THREADS], sq[8 * GN_MAX_THREADS];
   griddep_wait();
   griddep_launch_dependents();
   const int b = blockIdx.x / a.P, p = blockIdx.x - b * a.P;
   const int lo = p * a.rows, hi = min(a.S, lo + a.rows);
-  gn_block_stats<T, VEC, false>(a, static_cast<const T*>(a.X) + (int64_t)b * a.S * a.ldx, lo, hi, sum, sq, nullptr,
+  gn_block_stats<T, VEC, false, LARGE>(a, static_cast<const T*>(a.X) + (int64_t)b * a.S * a.ldx, lo, hi, sum, sq, nullptr,
                                 a.part + (int64_t)blockIdx.x * a.G);
 }
 
@@ -543,7 +567,7 @@ __global__ void __launch_bounds__(GN_SMALL_THREADS, 1) k_group_norm(const GroupN
   const int b = blockIdx.x / a.P, p = blockIdx.x - b * a.P;
   const int lo = p * a.rows, hi = min(a.S, lo + a.rows);
   const T* X = static_cast<const T*>(a.X) + (int64_t)b * a.S * a.ldx;
-  gn_block_stats<T, VEC, true>(a, X, lo, hi, sum, sq, kept, mine);
+  gn_block_stats<T, VEC, true, false>(a, X, lo, hi, sum, sq, kept, mine);
   GnApply<T, VEC, QUANT, true> t(a);                     // its loads on their way while the blocks meet
   __syncwarp();
   if (a.P > 1) cluster_sync_all();
