@@ -78,13 +78,17 @@ SVDQ_DEV void gn_params(const float* p, float other, int c, int C, float (&f)[8]
   }
 }
 
-// Eight channels from c of the row at p: one vector where every row starts on 16 bytes (VEC), else one by one;
-// channels past C are 0.  Plain loads: Y may be X.
+// Eight channels from c of the row at p.  VEC, every row on 16 bytes: as vectors.  Else from the aligned 16-byte pieces
+// that hold them, shifted into place (2 x 4096 x 637 in one
+// group: 18 us, 34 with loads and stores by the element); of a piece at least
+// one byte is the row's, so that no other piece is touched, and what lies past the row's end is never used.  Plain
+// loads: Y may be X.
 template <typename T, bool VEC>
 SVDQ_DEV void gn_load(const T* p, int c, int C, uint32_t (&w)[Elem<T>::kWords]) {
+  constexpr int W = Elem<T>::kWords;
   if constexpr (VEC) {
 #pragma unroll
-    for (int i = 0; i < Elem<T>::kWords / 4; ++i) {
+    for (int i = 0; i < W / 4; ++i) {
       const uint4 v = reinterpret_cast<const uint4*>(p + c)[i];
       w[4 * i] = v.x;
       w[4 * i + 1] = v.y;
@@ -92,10 +96,45 @@ SVDQ_DEV void gn_load(const T* p, int c, int C, uint32_t (&w)[Elem<T>::kWords]) 
       w[4 * i + 3] = v.w;
     }
   } else {
-    float f[8];
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p + c), end = reinterpret_cast<uintptr_t>(p + C);
+    const uint32_t off = (uint32_t)at & 15u;
+    const uint4* piece = reinterpret_cast<const uint4*>(at - off);
+    uint32_t q[W + 4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = c + i < C ? Elem<T>::to_f32(p[c + i]) : 0.0f;
-    Elem<T>::pack(f, w);
+    for (int i = 0; i <= W / 4; ++i) {
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (reinterpret_cast<uintptr_t>(piece + i) < end && (i < W / 4 || off)) v = piece[i];
+      q[4 * i] = v.x;
+      q[4 * i + 1] = v.y;
+      q[4 * i + 2] = v.z;
+      q[4 * i + 3] = v.w;
+    }
+#pragma unroll
+    for (int i = 0; i < W + 2; ++i) q[i] = off & 8u ? q[i + 2] : q[i];
+#pragma unroll
+    for (int i = 0; i < W + 1; ++i) q[i] = off & 4u ? q[i + 1] : q[i];
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = off & 2u ? __byte_perm(q[i], q[i + 1], 0x5432) : q[i];
+  }
+}
+
+// Eight channels at p, wherever it lies: the widest stores its alignment allows (the same for all of a row's threads).
+template <typename T>
+SVDQ_DEV void gn_store_any(T* p, const uint32_t (&w)[Elem<T>::kWords]) {
+  constexpr int W = Elem<T>::kWords;
+  const uint32_t off = (uint32_t)reinterpret_cast<uintptr_t>(p) & 15u;
+  if ((off & 7u) == 0u) {
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) reinterpret_cast<uint2*>(p)[i] = make_uint2(w[2 * i], w[2 * i + 1]);
+  } else if ((off & 3u) == 0u) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) reinterpret_cast<uint32_t*>(p)[i] = w[i];
+  } else {                                               // a 16-bit type on an odd element
+    uint16_t* h = reinterpret_cast<uint16_t*>(p);
+    h[0] = (uint16_t)w[0];
+#pragma unroll
+    for (int i = 0; i + 1 < W; ++i) *reinterpret_cast<uint32_t*>(h + 1 + 2 * i) = __byte_perm(w[i], w[i + 1], 0x5432);
+    h[2 * W - 1] = (uint16_t)(w[W - 1] >> 16);
   }
 }
 
@@ -117,6 +156,40 @@ SVDQ_DEV void gn_load(const T* p, int c, uint64_t policy, uint32_t (&w)[Elem<T>:
 
 // M2 is never negative but for rounding; a NaN stays one.
 SVDQ_DEV float gn_m2(float v) { return v < 0.0f ? 0.0f : v; }
+
+// (mean, M2) of each group from the n row slots' sums about the pivots, LANES lanes a group.
+template <typename T, int LANES>
+SVDQ_DEV void gn_group_sums(const GroupNormArgs& a, const T* X, int lo, int hi, int n, const float* sum, const float* sq,
+                            float2* out) {
+  constexpr int kGroups = 32 / LANES;                    // a warp's groups at a time
+  const int width = 8 * a.nv, cg = a.C / a.G, lane = threadIdx.x & 31;
+  const float count = (float)(hi - lo) * (float)cg, inv = 1.0f / count;
+  for (int g0 = kGroups * (threadIdx.x >> 5); g0 < a.G; g0 += kGroups * (blockDim.x >> 5)) {   // uniform over a warp
+    const int g = min(g0 + lane / LANES, a.G - 1);
+    const float pivot = Elem<T>::to_f32(X[(int64_t)lo * a.ldx + g * cg]);
+    float s1 = 0.0f, q1 = 0.0f;
+#pragma unroll 4                                         // 64 loads in flight (2 x 1024 x 1280: 9.0 us, 9.6 without)
+    for (int i = g * cg + lane % LANES; i < (g + 1) * cg; i += LANES) {
+      float s[8], q[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        s[k] = k < n ? sum[i + k * width] : 0.0f;
+        q[k] = k < n ? sq[i + k * width] : 0.0f;
+      }
+      s1 += ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
+      q1 += ((q[0] + q[1]) + (q[2] + q[3])) + ((q[4] + q[5]) + (q[6] + q[7]));
+    }
+#pragma unroll
+    for (int o = LANES / 2; o; o >>= 1) {
+      s1 += __shfl_xor_sync(0xFFFFFFFFu, s1, o);
+      q1 += __shfl_xor_sync(0xFFFFFFFFu, q1, o);
+    }
+    if (lane % LANES == 0 && g0 + lane / LANES < a.G) {
+      const float d = s1 * inv;
+      out[g] = make_float2(pivot + d, gn_m2(q1 - d * s1));
+    }
+  }
+}
 
 // First pass over the block's rows lo..hi: (mean, M2) of each group to out (shared or global memory).  sum and
 // sq: 8 floats a thread each.  KEEP: the rows also go to `kept` (row by row, nv vectors).  LARGE: the tensor is larger
@@ -196,32 +269,10 @@ SVDQ_DEV void gn_block_stats(const GroupNormArgs& a, const T* X, int lo, int hi,
     n = h;
   }
   __syncthreads();
-  // each group's channels and slots, by eight lanes
-  const float count = (float)(hi - lo) * (float)cg, inv = 1.0f / count;
-  for (int g0 = 4 * (threadIdx.x >> 5); g0 < a.G; g0 += blockDim.x >> 3) {     // uniform over a warp
-    const int g = min(g0 + (lane >> 3), a.G - 1);
-    const float pivot = Elem<T>::to_f32(X[(int64_t)lo * a.ldx + g * cg]);
-    float s1 = 0.0f, q1 = 0.0f;
-    for (int i = g * cg + (lane & 7); i < (g + 1) * cg; i += 8) {
-      float s[8], q[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        s[k] = k < n ? sum[i + k * width] : 0.0f;
-        q[k] = k < n ? sq[i + k * width] : 0.0f;
-      }
-      s1 += ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
-      q1 += ((q[0] + q[1]) + (q[2] + q[3])) + ((q[4] + q[5]) + (q[6] + q[7]));
-    }
-#pragma unroll
-    for (int o = 4; o; o >>= 1) {
-      s1 += __shfl_xor_sync(0xFFFFFFFFu, s1, o);
-      q1 += __shfl_xor_sync(0xFFFFFFFFu, q1, o);
-    }
-    if ((lane & 7) == 0 && g0 + (lane >> 3) < a.G) {
-      const float d = s1 * inv;
-      out[g] = make_float2(pivot + d, gn_m2(q1 - d * s1));
-    }
-  }
+  // each group's channels and slots: by eight lanes, or a warp where few groups have many channels (2 x 4096 x 640 in
+  // one group: 10.4 us, 13.1 with eight lanes)
+  if (a.G <= 4) gn_group_sums<T, 32>(a, X, lo, hi, n, sum, sq, out);
+  else gn_group_sums<T, 8>(a, X, lo, hi, n, sum, sq, out);
 }
 
 // Running merge of blocks' (n, mean, M2) against a common base: n, sum n (mean - base), sum n (mean - base)^2, M2.
@@ -360,6 +411,10 @@ SVDQ_DEV void gn_apply_loop(const GroupNormArgs& a, GnApply<T, VEC, QUANT, KEEP>
               if (a.streaming) __stcs(reinterpret_cast<uint4*>(p) + i, d);
               else reinterpret_cast<uint4*>(p)[i] = d;
             }
+          } else if (c + 8 <= a.C) {
+            uint32_t o[W];
+            Elem<T>::pack(f, o);
+            gn_store_any<T>(p, o);
           } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
