@@ -284,3 +284,94 @@ def test_work_queued_before_and_after_the_layer_is_ordered():
         X.neg_()
         y1 = call(X, W)
         assert torch.equal(y0, want[0]) and torch.equal(y1, want[1])
+
+
+@pytest.mark.parametrize("M,N,K,pad,smooth", [
+    (1, 5, 16, 0, True), (1, 128, 144, 8, False), (1, 5120, 1280, 0, True), (2, 1001, 2064, 16, True),
+    (1, 4096, 4096, 0, False), (3, 320, 4096, 0, True), (1, 1288, 12288, 0, True), (1, 12288, 4096, 0, True),
+    (4, 256, 1280, 8, True), (7, 640, 640, 0, False), (8, 129, 1040, 0, True), (9, 64, 320, 0, True),
+    (10, 1280, 320, 0, True), (16, 1280, 256, 0, True), (16, 1280, 320, 0, True), (16, 2048, 1040, 0, True), (17, 320, 320, 0, True), (1, 64, 20480, 0, True)])
+@pytest.mark.parametrize("kind", TYPES)
+def test_few_tokens_give_the_bits_of_the_two_calls(M, N, K, pad, smooth, kind):
+    """The one-call form may quantize inside its GEMM; integers are exact, so its results are the same bits.
+    Rows of zeros, of tiny values and (with more than two) one infinity and one NaN are among them."""
+    C = _lib()
+    g = torch.Generator(device="cuda").manual_seed(M * 1000 + K)
+    full = (torch.randn(M, K + pad, device="cuda", generator=g) * 4).to(TYPES[kind])
+    X = full[:, :K]
+    if M > 2:
+        X[1] = 0.0
+        X[2, K - 1] = float("inf")
+    if M > 3:
+        X[3, K // 2] = float("nan")
+        X[3, 0] = float("-inf")
+    if M > 4:
+        X[4] = 2.0 ** -120 if kind != "fp16" else 2.0 ** -24
+    inv_s = torch.rand(K, device="cuda", generator=g) + 0.5 if smooth else None
+    W = torch.randint(-127, 128, (N, K), device="cuda", generator=g, dtype=torch.int8)
+    sw = torch.rand(N, device="cuda", generator=g)
+    bias = torch.randn(N, device="cuda", generator=g) if smooth else None
+    q = torch.empty(M, K, dtype=torch.int8, device="cuda")
+    sx = torch.empty(M, device="cuda")
+    want = torch.empty(M, N, device="cuda")
+    C.svdq_quantize_act_i8(X, M, K, inv_s, q, sx)
+    C.svdq_linear_i8(q, sx, W, sw, bias, want, M, N, K)
+    ws = torch.empty(C.svdq_forward_i8_workspace_bytes(M, K), dtype=torch.uint8, device="cuda")
+    for ypad in (0, 3):
+        out = torch.full((M, N + ypad), 7.0, device="cuda")
+        for _ in range(2):
+            C.svdq_forward_i8(X, M, K, inv_s, W, sw, bias, out[:, :N], N, ws)
+        torch.cuda.synchronize()
+        assert C.svdq_get_device_error() == (0, 0)
+        assert torch.equal(out[:, :N].nan_to_num(1e30), want.nan_to_num(1e30))
+        assert torch.equal(out[:, :N].isnan(), want.isnan())
+        assert bool((out[:, N:] == 7.0).all())
+
+
+def test_output_over_the_input():
+    """Y on X's memory: X is read whole before Y is written."""
+    C = _lib()
+    K = 1280
+    g = torch.Generator(device="cuda").manual_seed(5)
+    X = torch.randn(2, K, device="cuda", generator=g).to(torch.bfloat16)
+    W = torch.randint(-127, 128, (K, K), device="cuda", generator=g, dtype=torch.int8)
+    sw = torch.rand(K, device="cuda", generator=g)
+    ws = torch.empty(C.svdq_forward_i8_workspace_bytes(2, K), dtype=torch.uint8, device="cuda")
+    want = torch.empty_like(X)
+    C.svdq_forward_i8(X, 2, K, None, W, sw, None, want, K, ws)
+    for _ in range(20):
+        Y = X.clone()
+        C.svdq_forward_i8(Y, 2, K, None, W, sw, None, Y, K, ws)
+        assert torch.equal(Y, want)
+
+
+def test_rows_that_graphs_and_neighbours_share_with_few_tokens():
+    """A chain of one-token layers, each reading the row that the launch before it wrote, in a replayed graph."""
+    C = _lib()
+    K = 1024
+    g = torch.Generator(device="cuda").manual_seed(6)
+    W = [torch.randint(-127, 128, (K, K), device="cuda", generator=g, dtype=torch.int8) for _ in range(6)]
+    sw = torch.full((K,), 1.0 / (73.0 * 32.0), device="cuda")
+    ws = torch.empty(C.svdq_forward_i8_workspace_bytes(1, K), dtype=torch.uint8, device="cuda")
+    X = torch.randn(1, K, device="cuda", generator=g).to(torch.bfloat16)
+    bufs = [torch.empty(1, K, device="cuda", dtype=torch.bfloat16) for _ in W]
+
+    def chain(sync):
+        x = X
+        for w, y in zip(W, bufs):
+            C.svdq_forward_i8(x, 1, K, None, w, sw, None, y, K, ws)
+            if sync:
+                torch.cuda.synchronize()
+            x = y
+        return x
+
+    want = chain(True).clone()
+    G = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(G):
+        chain(False)
+    for _ in range(50):
+        for b in bufs:
+            b.zero_()
+        G.replay()
+        assert torch.equal(bufs[-1], want)
+        assert torch.equal(chain(False), want)

@@ -5,6 +5,8 @@
 // Both kernels run tcgen05.mma.kind::i8 on 128-byte chunks of K that TMA lands in 128-byte swizzled
 // tiles (chunks past K and rows past M or N are zero-filled and add nothing).
 #pragma once
+#include <type_traits>
+
 #include "int8.cuh"
 #include "tc_i8.cuh"
 
@@ -24,6 +26,9 @@ struct LinearI8Args {
   int nt;               // columns (pair kernel) or tokens (split kernel) of a tile
   int stages;           // ring slots (split kernel)
   int w_early;          // split kernel: the weight may be read before griddepcontrol.wait
+  const void* X;        // split kernel that quantizes its tokens itself: their rows and smoothing factors
+  int64_t ldx;
+  const float* inv_s;
 };
 
 SVDQ_DEV float i8_dequant(int acc, float sx, float sw, float bias) {
@@ -335,21 +340,78 @@ constexpr int LS_THREADS = 256;
 constexpr int LS_A_BYTES = 128 * 128;
 constexpr int LS_TAIL_BYTES = 256 + 1024;                 // barriers, then the tile's token scales
 
-__global__ void __launch_bounds__(LS_THREADS) k_linear_i8_split(
+// One or a few tokens quantized by the GEMM itself (XT their type; int8_t: they come as codes): every CTA reads
+// all of their rows for the maxima (L2 holds them, and a cluster barrier to share them would cost more), then writes the codes of its
+// own K range where TMA would have put them, while the first weight boxes are on their way.  One launch instead of two.
+constexpr int LS_FUSED_TOKENS = 16;                       // nt; a chunk of 128 of K is 16 rows of 128 bytes
+constexpr int LS_FUSED_CHUNK = LS_FUSED_TOKENS * 128;
+constexpr int LS_FUSED_THREADS = 512;
+template <typename XT>
+__host__ __device__ constexpr int split_threads() {
+  return std::is_same<XT, int8_t>::value ? LS_THREADS : LS_FUSED_THREADS;
+}
+// All threads.  A half warp takes one of the rows' chunks of 128 columns, whose x_hat stays in registers between the
+// maximum and the codes (with two or four chunks a half warp, code that runs once and is not in the instruction cache yet
+// cost 0.2 and 0.6 us).  top: zeroes; codes: the CTA's chunks, k_lo to k_hi.
+template <typename T>
+SVDQ_DEV void quantize_tokens(const LinearI8Args& a, int k_lo, int k_hi, uint32_t* top, float* sxs, uint8_t* codes) {
+  const int nkt = (a.K + 127) >> 7, l = threadIdx.x & 15;
+  const int unit = threadIdx.x >> 4, row = unit / nkt, chunk = unit - row * nkt, v = chunk * 16 + l;
+  const bool in = row < a.M && 8 * v < a.K;
+  uint32_t w[Elem<T>::kWords];
+  float4 s0 = make_float4(1.f, 1.f, 1.f, 1.f), s1 = s0;
+#pragma unroll
+  for (int i = 0; i < Elem<T>::kWords; ++i) w[i] = 0u;
+  if (in) load8(static_cast<const T*>(a.X) + (int64_t)row * a.ldx + 8 * v, w);
+  if (in && a.inv_s) {
+    s0 = __ldg(reinterpret_cast<const float4*>(a.inv_s) + 2 * v);
+    s1 = __ldg(reinterpret_cast<const float4*>(a.inv_s) + 2 * v + 1);
+  }
+  float f[8], m = 0.0f;
+  Elem<T>::unpack(w, f);
+  const float2 xh[4] = {mul_f32x2(make_float2(f[0], f[1]), make_float2(s0.x, s0.y)),
+                        mul_f32x2(make_float2(f[2], f[3]), make_float2(s0.z, s0.w)),
+                        mul_f32x2(make_float2(f[4], f[5]), make_float2(s1.x, s1.y)),
+                        mul_f32x2(make_float2(f[6], f[7]), make_float2(s1.z, s1.w))};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = max_abs(m, xh[i].x, xh[i].y);
+  uint32_t b = __float_as_uint(m);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) b = umax(b, __shfl_xor_sync(0xFFFFFFFFu, b, o));
+  if (l == 0 && row < a.M) atomicMax(top + row, b);
+  __syncthreads();
+  if (row >= a.M) return;
+  if (chunk == 0 && l == 0) sxs[row] = i8_scale_or_mul(top[row], true);
+  if (chunk < k_lo || chunk >= k_hi) return;
+  const float mul = i8_scale_or_mul(top[row], false);
+  const uint2 c = i8_codes(xh, mul);
+  *reinterpret_cast<uint2*>(codes + (chunk - k_lo) * LS_FUSED_CHUNK + row * 128 + ((((l >> 1) ^ row) & 7) << 4) +
+                            8 * (l & 1)) = mul == 0.0f ? make_uint2(0u, 0u) : c;
+}
+
+// chunks of 128 of K that a CTA of a cluster of `split` has at most
+__host__ __device__ __forceinline__ int code_chunks(int K, int split) { return (((K + 127) >> 7) + split - 1) / split; }
+
+template <typename XT>
+__global__ void __launch_bounds__(split_threads<XT>()) k_linear_i8_split(
     const __grid_constant__ CUtensorMap tm_w,    // uint8 {K, N}, box {128, 128}, SW128
-    const __grid_constant__ CUtensorMap tm_x,    // uint8 {K, M}, box {128, nt}, SW128
+    const __grid_constant__ CUtensorMap tm_x,    // uint8 {K, M}, box {128, nt}, SW128 (codes only)
     const LinearI8Args a, const int split) {
+  constexpr bool CODES = std::is_same<XT, int8_t>::value;
+  constexpr int THREADS = split_threads<XT>();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int stage_bytes = LS_A_BYTES + a.nt * 128;
+  const int stage_bytes = LS_A_BYTES + (CODES ? a.nt * 128 : 0);
   const int ring = max(a.stages * stage_bytes, a.nt * 512);            // the sums take the ring's place
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + ring);
+  // 16 tokens' codes of the CTA's K range lie past the ring where the kernel makes them
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + ring + (CODES ? 0 : code_chunks(a.K, split) * LS_FUSED_CHUNK));
   uint64_t* empty = full + a.stages;
   uint64_t* acc_full = empty + a.stages;
   uint64_t* drain = acc_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  float* sxs = reinterpret_cast<float*>(smem + ring + 256);
+  float* sxs = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(full) + 256);
+  uint32_t* top = reinterpret_cast<uint32_t*>(sxs + 128);              // the tokens' largest magnitudes
 
   const int warp = (int)warp_uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int rank = split > 1 ? (int)warp_uniform(cluster_rank()) : 0;
@@ -370,8 +432,9 @@ __global__ void __launch_bounds__(LS_THREADS) k_linear_i8_split(
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tm_w);
-    tma_prefetch_desc(&tm_x);
+    if (CODES) tma_prefetch_desc(&tm_x);
   }
+  if (!CODES && threadIdx.x < LS_FUSED_TOKENS) top[threadIdx.x] = 0u;
   if (warp == 1) {
     tmem_alloc(tmem_slot, cols);
     tmem_relinquish();
@@ -382,9 +445,10 @@ __global__ void __launch_bounds__(LS_THREADS) k_linear_i8_split(
   const uint32_t tbase = warp_uniform(*tmem_slot);
   int issued = 0;                                                      // copying warp: ring rounds begun
 
+  if (!CODES) griddep_wait();
+  const int ahead = !CODES || a.w_early ? min(nk, a.stages) : 0;
   if (warp == 0) {
-    const int yw = nb * 128, yx = mb * a.nt;
-    const int ahead = a.w_early ? min(nk, a.stages) : 0;
+    const int yw = nb * 128;
     // The weight's first boxes may come before the wait where the kernel launched just before this one has
     // itself waited for all earlier work (svdq_forward_i8's quantizer): nothing in flight writes the weight.
     for (int kt = 0; kt < ahead; ++kt) {
@@ -397,17 +461,26 @@ __global__ void __launch_bounds__(LS_THREADS) k_linear_i8_split(
       __syncwarp();
     }
     issued = ahead;
-    griddep_wait();
+  }
+  if constexpr (!CODES) {
+    griddep_launch_dependents();
+    quantize_tokens<XT>(a, k_lo, k_hi, top, sxs, smem + ring);
+    fence_proxy_async();                                                // the MMAs read the codes
+    __syncthreads();
+  }
+  if (warp == 0) {
+    const int yw = nb * 128, yx = mb * a.nt;
+    if (CODES) griddep_wait();
     int s = 0;
-    uint32_t phase = 1;
-    for (int kt = 0; kt < nk; ++kt) {
+    uint32_t phase = CODES ? 1 : 0;                                     // !CODES: from the ring's second round on
+    for (int kt = CODES ? 0 : ahead; kt < nk; ++kt) {
       uint8_t* dst = smem + s * stage_bytes;
       if (kt >= ahead && !mbar_wait_warp(&empty[s], phase, tmo, abort_flag, 0x531)) break;
       if (elect_one()) {
         if (kt >= ahead) mbar_arrive_expect_tx(&full[s], (uint32_t)stage_bytes);
         if (SVDQ_CHECK_OK((uint32_t)(dst - smem_raw) + stage_bytes <= dyn_smem_bytes(), 0x5c3)) {
           if (kt >= ahead) tma_load_2d(dst, &tm_w, &full[s], (k_lo + kt) * 128, yw);
-          tma_load_2d(dst + LS_A_BYTES, &tm_x, &full[s], (k_lo + kt) * 128, yx);
+          if (CODES) tma_load_2d(dst + LS_A_BYTES, &tm_x, &full[s], (k_lo + kt) * 128, yx);
         }
       }
       __syncwarp();
@@ -425,7 +498,8 @@ __global__ void __launch_bounds__(LS_THREADS) k_linear_i8_split(
     for (; kt < nk; ++kt) {
       if (!mbar_wait_warp(&full[s], phase, tmo, abort_flag, 0x532)) break;
       tc_fence_after();
-      const uint64_t ad = desc0 + (uint64_t)(s * (stage_bytes / 16)), bd = ad + LS_A_BYTES / 16;
+      const uint64_t ad = desc0 + (uint64_t)(s * (stage_bytes / 16));
+      const uint64_t bd = CODES ? ad + LS_A_BYTES / 16 : desc0 + (uint64_t)((ring + kt * LS_FUSED_CHUNK) / 16);
       if (elect_one()) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) tc_mma_i8(tbase, ad + 2 * j, bd + 2 * j, idesc, (kt | j) != 0 ? 1u : 0u);
@@ -448,9 +522,11 @@ __global__ void __launch_bounds__(LS_THREADS) k_linear_i8_split(
   __syncwarp();
 
   // ------------------------------------------------------------------ epilogue ---
-  if (warp != 0) griddep_wait();                         // the copying warp has waited
-  __syncwarp();
-  griddep_launch_dependents();
+  if (CODES) {
+    if (warp != 0) griddep_wait();                       // the copying warp has waited
+    __syncwarp();
+    griddep_launch_dependents();
+  }
   const int tokens = min(a.nt, a.M - mb * a.nt);
   const int n = nb * 128 + 4 * lane;                     // four channels a lane
   float s4[4], b4[4];
@@ -459,7 +535,8 @@ __global__ void __launch_bounds__(LS_THREADS) k_linear_i8_split(
     s4[i] = n + i < a.N ? __ldg(a.sw + n + i) : 0.0f;
     b4[i] = a.bias && n + i < a.N ? __ldg(a.bias + n + i) : 0.0f;
   }
-  for (int t = threadIdx.x; t < tokens; t += LS_THREADS) sxs[t] = __ldg(a.sx + mb * a.nt + t);
+  if (CODES)
+    for (int t = threadIdx.x; t < tokens; t += THREADS) sxs[t] = __ldg(a.sx + mb * a.nt + t);
   const bool got = __all_sync(0xFFFFFFFFu, mbar_wait(acc_full, 0, tmo, abort_flag, 0x533));
   if (!got && warp == 0 && lane == 0) {                  // let the copies in flight land before the CTA exits
     int never = 0;
@@ -490,7 +567,7 @@ __global__ void __launch_bounds__(LS_THREADS) k_linear_i8_split(
   }
   const uint32_t mine = smem_u32(part) + 16u * (uint32_t)lane;
 #pragma unroll 4
-  for (int t = rank + split * warp; t < tokens; t += split * (LS_THREADS / 32)) {
+  for (int t = rank + split * warp; t < tokens; t += split * (THREADS / 32)) {
     int4 acc = make_int4(0, 0, 0, 0);
     for (int r = 0; r < split; ++r) {
       const int4 v = split > 1 ? ld_cluster_v4(map_to_rank(mine + 512u * (uint32_t)t, (uint32_t)r))

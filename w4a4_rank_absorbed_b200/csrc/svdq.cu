@@ -596,13 +596,52 @@ LinearI8Plan plan_linear_i8(int64_t M, int64_t N, int64_t K, int sms) {
   return last.plan;
 }
 
+// Whether svdq_forward_i8 leaves the quantizing to the split kernel: where a half warp a chunk of 128 columns is enough.
+// Measured, one launch against two, weights from HBM: 1 x 12288 of K = 4096 11.9 and 13.7 us, 1 x 4096 of K = 4096
+// 6.7 and 8.5, 1 x 5120 of K = 1280 4.7 and 5.6, 4 x 640 of K = 640 3.9 and 5.0.  With twice the threads, and so twice
+// the limit, 1 x 5120 of K = 1280 took 5.9 (fewer CTAs an SM); with two chunks a half warp 2 x 4096 of K = 4096 9.0
+// against 8.5.
+bool fuse_tokens_i8(const LinearI8Plan& p, int64_t M, int64_t K) {
+  return !p.pair && M <= LS_FUSED_TOKENS && M * ((K + 127) / 128) <= LS_FUSED_THREADS / 16;
+}
+
+// Whether [a, a + rows) and [b, b + rows) may share bytes.
+bool may_overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+size_t rows_bytes(int64_t rows, int64_t width, int64_t ld, int type) {
+  return ((size_t)(rows - 1) * (size_t)ld + (size_t)width) * dtype_size(type);
+}
+
+template <typename T>
+svdq_status launch_fused_i8(int dev, const LinearI8Plan& p, LinearI8Args& a, const int8_t* Wq,
+                            cudaStream_t s) {
+  static std::atomic<bool> attr[kMaxDevices];
+  CUtensorMap tm_w;
+  if (!make_map_2d(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, Wq, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.K, 128, 128))
+    return SVDQ_ERR_CUDA;
+  const int per = code_chunks(a.K, p.split);
+  a.nt = LS_FUSED_TOKENS;
+  a.stages = std::min(per, 6);
+  constexpr int most = 6 * LS_A_BYTES + LS_FUSED_THREADS / 16 * LS_FUSED_CHUNK + LS_TAIL_BYTES + 1024;
+  const size_t smem = (size_t)a.stages * LS_A_BYTES + per * LS_FUSED_CHUNK + LS_TAIL_BYTES + 1024;
+  svdq_status st;
+  if ((st = allow_smem(k_linear_i8_split<T>, dev, attr, most)) != SVDQ_OK) return st;
+  if (launch_pdl(k_linear_i8_split<T>, dim3((unsigned)(((int64_t)a.N + 127) / 128 * p.split)), dim3(LS_FUSED_THREADS), smem, s,
+                 p.split, tm_w, tm_w, a, p.split) != cudaSuccess)
+    return launch_failed();
+  return launch_status();
+}
+
 // w_early: the kernel before this one on the stream is a quantizer of this library, which has waited for
 // everything before it, so the weight may be read while it still runs.
 svdq_status launch_linear_i8(int dev, DevInfo* d, const int8_t* Xq, const float* sx, const int8_t* Wq,
                              const float* sw, const float* bias, void* Y, int y_type, int64_t ldy, int64_t M,
                              int64_t N, int64_t K, int w_early, cudaStream_t s) {
   const LinearI8Plan p = plan_linear_i8(M, N, K, d->sms);
-  LinearI8Args a;
+  LinearI8Args a = {};
   a.sx = sx;
   a.sw = sw;
   a.bias = bias;
@@ -637,8 +676,8 @@ svdq_status launch_linear_i8(int dev, DevInfo* d, const int8_t* Xq, const float*
   const int per = (int)(((K + 127) / 128 + p.split - 1) / p.split);
   a.stages = std::min(per, 100 * 1024 / stage);
   const size_t smem = (size_t)std::max(a.stages * stage, p.nt * 512) + LS_TAIL_BYTES + 1024;
-  if ((st = allow_smem(k_linear_i8_split, dev, g_split_attr, 100 * 1024 + LS_TAIL_BYTES + 1024)) != SVDQ_OK) return st;
-  if (launch_pdl(k_linear_i8_split, dim3((unsigned)((N + 127) / 128 * p.split), (unsigned)((M + p.nt - 1) / p.nt)),
+  if ((st = allow_smem(k_linear_i8_split<int8_t>, dev, g_split_attr, 100 * 1024 + LS_TAIL_BYTES + 1024)) != SVDQ_OK) return st;
+  if (launch_pdl(k_linear_i8_split<int8_t>, dim3((unsigned)((N + 127) / 128 * p.split), (unsigned)((M + p.nt - 1) / p.nt)),
                  dim3(LS_THREADS), smem, s, p.split, tm_w, tm_x, a, p.split) != cudaSuccess)
     return launch_failed();
   return launch_status();
@@ -1027,6 +1066,26 @@ svdq_status svdq_forward_i8(const void* X, int x_type, int64_t ldx, const float*
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int8_t* Xq = static_cast<int8_t*>(workspace);           // M x K codes (K % 16 == 0), then the M scales
   float* sx = reinterpret_cast<float*>(Xq + (size_t)M * (size_t)K);
+  const LinearI8Plan p = plan_linear_i8(M, N, K, d->sms);
+  // (One kernel for both reads X while it writes Y; the two kernels do not.)
+  if (fuse_tokens_i8(p, M, K) && !may_overlap(X, rows_bytes(M, K, ldx, x_type), Y, rows_bytes(M, N, ldy, y_type))) {
+    LinearI8Args a = {};
+    a.sw = sw;
+    a.bias = bias;
+    a.Y = Y;
+    a.y_type = y_type;
+    a.y_vec = y_vector(Y, y_type, ldy);
+    a.ldy = ldy;
+    a.M = (int)M;
+    a.N = (int)N;
+    a.K = (int)K;
+    a.X = X;
+    a.ldx = ldx;
+    a.inv_s = inv_s;
+    if (x_type == SVDQ_BF16) return launch_fused_i8<__nv_bfloat16>(dev, p, a, Wq, s);
+    if (x_type == SVDQ_FP16) return launch_fused_i8<__half>(dev, p, a, Wq, s);
+    return launch_fused_i8<float>(dev, p, a, Wq, s);
+  }
   if ((st = launch_quantize_i8(d, X, x_type, ldx, M, K, inv_s, Xq, sx, s)) != SVDQ_OK) return st;
   return launch_linear_i8(dev, d, Xq, sx, Wq, sw, bias, Y, y_type, ldy, M, N, K, 1, s);
 }

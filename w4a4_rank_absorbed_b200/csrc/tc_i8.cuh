@@ -109,6 +109,9 @@ SVDQ_DEV void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// Makes this thread's stores to shared memory visible to copies and MMAs issued after the next barrier.
+SVDQ_DEV void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
 // 2-D tiled load into this CTA's shared memory, completion counted on a barrier of the pair (a
 // shared::cluster address: the leader's).
 SVDQ_DEV void tma_load_2d_pair(void* dst, const CUtensorMap* m, uint32_t bar, int32_t x, int32_t y) {
