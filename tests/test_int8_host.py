@@ -93,6 +93,8 @@ def test_rows_of_strided_tensors():
     for bad, rows, width in ((t[:, :4, :], 16, 32),              # two pitches
                              (t.transpose(1, 2), 128, 6),        # columns not contiguous
                              (t[0, :1].expand(6, 32), 6, 32),    # the same row again and again
+                             (t[:, :1].expand(4, 3, 32), 12, 32), (t[:1].expand(4, 6, 32), 24, 32),
+                             (t[:, :1, :1].expand(4, 3, 1), 12, 1), (t[:, :, :1].expand(4, 6, 5), 24, 5),
                              (t, 23, 32), (t, 24, 31)):
         with pytest.raises(ValueError):
             C._rows(bad, rows, width, -1, "t")
@@ -128,6 +130,11 @@ def test_layer_arguments():
     with pytest.raises(ValueError):
         W8A8Linear.from_state_dict({"K": 16, "N": 4, "Wq": torch.zeros(4, 15, dtype=torch.int8), "sw": torch.zeros(4),
                                     "inv_s": None, "bias": None}, device="cpu")
+    layer = W8A8Linear.from_state_dict({"K": 16, "N": 4, "Wq": torch.zeros(4, 16, dtype=torch.int8), "sw": torch.zeros(4),
+                                        "inv_s": None, "bias": None}, device="cpu")
+    for codes in (torch.zeros(2, 32, dtype=torch.int8), torch.zeros(32, dtype=torch.int8)):
+        with pytest.raises(ValueError, match="Xq must be"):
+            layer.gemm(codes, torch.zeros(2), torch.zeros(2, 4))
 
 
 def test_calibration_smooths():

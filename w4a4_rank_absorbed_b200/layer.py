@@ -371,6 +371,7 @@ class W8A8Linear:
                 self.bias = None if data.bias is None else data.bias.to(dev, torch.float32).contiguous()
             if s is not None:
                 torch.cuda.current_stream(dev).wait_stream(s)
+                _used_here(self.Wq, self.sw, self.inv_s, self.bias)
 
     def state_dict(self) -> Dict[str, object]:
         """The packed layer as host tensors and sizes (W8A8Linear.from_state_dict rebuilds it)."""
@@ -424,6 +425,8 @@ class W8A8Linear:
     def gemm(self, Xq: torch.Tensor, sx: torch.Tensor, Y: torch.Tensor, stream=None) -> torch.Tensor:
         for t, name in ((Xq, "Xq"), (sx, "sx"), (Y, "Y")):
             check_device(t, self.device, name)
+        if Xq.dim() != 2 or Xq.shape[1] != self.K:
+            raise ValueError(f"Xq must be [rows, {self.K}], got {tuple(Xq.shape)}")
         with torch.cuda.device(self.device), _on_stream(stream, self.device):
             _C.svdq_linear_i8(Xq, sx, self.Wq, self.sw, self.bias, Y, Xq.shape[0], self.N, self.K)
             if stream is not None:

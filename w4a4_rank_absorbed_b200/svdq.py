@@ -433,18 +433,18 @@ def _rows(t, rows: int, width: int, dev: int, name: str):
     if t.is_contiguous():
         return t.data_ptr(), ty, width
     st = t.stride()
-    ld = 0                                         # the pitch: the innermost leading axis longer than 1 gives it
+    ld = None                                      # the pitch: the innermost leading axis longer than 1 gives it
     expect = 0
     for i in range(len(shape) - 2, -1, -1):
         if shape[i] != 1:
-            if ld == 0:
+            if ld is None:
                 ld = expect = st[i]
             if st[i] != expect:
                 raise ValueError(f"{name}: its rows are not at one pitch (strides {st})")
         expect *= shape[i]
-    if (width > 1 and st[-1] != 1) or (rows > 1 and ld < width):
+    if (width > 1 and st[-1] != 1) or (rows > 1 and ld < width):     # (a broadcast axis: 0)
         raise ValueError(f"{name}: expected rows of contiguous elements (strides {st})")
-    return t.data_ptr(), ty, max(ld, width)
+    return t.data_ptr(), ty, max(ld or 0, width)
 
 
 def _cuda_index(t, name: str) -> int:
