@@ -118,6 +118,48 @@ def test_means_far_from_zero(offset):
     _check(_run(X, 1, 2000, 64, 8, gamma, beta, 1e-5, "none"), X, 8, gamma, beta, 1e-5, "none", "fp32")
 
 
+def pivot_bound(x, G, eps, far):
+    """(exact y, largest error): as value_bound, for groups of which the values that `far` marks lie far from all others,
+    which spread by R about the mean c of those others.  The pivot is one of the others (the median of three of the
+    block's, of which one at most is far), so sums of squares about it are of positive numbers, Q <= sum (|x - c| + R)^2,
+    each off by k U of itself after k steps one after another: the variance by k U Q / N and twice the mean's error
+    squared.  Sums of x - p: k U A / N, A = sum (|x - c| + R).  k = 512: a thread's run of rows, then trees.  Blocks
+    merge about the first one's mean, by 8 more steps of values up to D (their means) and U of D each."""
+    g = x.astype(np.float64).reshape(*x.shape[:2], G, x.shape[2] // G)
+    near = ~far.reshape(g.shape)
+    mean = g.mean(axis=(1, 3), keepdims=True)
+    var = ((g - mean) ** 2).mean(axis=(1, 3), keepdims=True)
+    n = near.sum(axis=(1, 3), keepdims=True)
+    c = np.where(near, g, 0.0).sum(axis=(1, 3), keepdims=True) / n
+    R = np.where(near, np.abs(g - c), 0.0).max(axis=(1, 3), keepdims=True)
+    D = np.abs(g - c).max(axis=(1, 3), keepdims=True)
+    k = 512
+    Q = ((np.abs(g - c) + R) ** 2).mean(axis=(1, 3), keepdims=True)
+    A = (np.abs(g - c) + R).mean(axis=(1, 3), keepdims=True)
+    em = k * U * A + 8 * U * D + U * np.abs(mean)
+    er = 0.5 * (k * U * Q + 2 * em ** 2 + 4 * em * A) / (var + eps) + 4 * U
+    rstd = 1.0 / np.sqrt(var + eps)
+    z = np.abs(g - mean) * rstd
+    y = ((g - mean) * rstd).reshape(x.shape)
+    return y, (em * rstd + z * (er + 6 * U)).reshape(x.shape) + 2 * U * np.abs(y)
+
+
+@pytest.mark.parametrize("where", ["value", "row", "last row", "middle row"])
+@pytest.mark.parametrize("B,S,C,G", [(1, 200000, 64, 16), (2, 30000, 128, 8), (1, 3000, 1024, 1), (1, 300, 48, 6), (1, 9, 1024, 1024)])
+def test_values_far_from_the_others(B, S, C, G, where):
+    """One value, or one row, thousands of deviations away, at the places a pivot may be taken from."""
+    r = np.random.default_rng(S)
+    x = r.normal(size=(B, S, C)).astype(np.float32)
+    far = np.zeros(x.shape, dtype=bool)
+    row = {"value": 0, "row": 0, "last row": S - 1, "middle row": S // 2}[where]
+    far[:, row, ::C // G if where == "value" else 1] = True
+    x[far] += 3000.0
+    Y = _run(torch.from_numpy(x).cuda(), B, S, C, G, None, None, 1e-5, "none")
+    y, e = pivot_bound(x, G, 1e-5, far)
+    err = np.abs(Y.double().cpu().numpy() - y)
+    assert np.all(err <= e), float((err / e).max())
+
+
 def test_constant_groups_and_zero_eps():
     X = torch.full((1, 50, 32), 5.0, device="cuda")
     beta = np.arange(32, dtype=np.float32)

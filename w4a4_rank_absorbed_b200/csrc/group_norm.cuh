@@ -11,11 +11,14 @@
 //                  Each block of the first leaves (mean, M2) of its rows per group, each block of the second
 //                  merges those of its sample: nothing needs clearing, no block waits for another.
 // The order of every sum is fixed.
+// Measured: a megapixel of 128 bf16 channels with SiLU 139 us, 0.8 GB moved, 0.90 of the copy bandwidth; 2 x 4096 x 640
+// 11.2 us (9.7 without SiLU; two launches' latencies are 6 of it); 64 x 320 6.7 us (one launch).  Codes: 2 x 1024 x 1280
+// 10.6 us, 16384 x 320 15.6 us (issue-bound: of a row's 64 threads 40 hold a vector).
 //
 // Statistics: a thread owns 8 consecutive channels (a 16-byte vector of a 16-bit type) of every rp-th row,
-// whichever groups they fall in, and sums x - p and its square per channel, p the first channel of the group in the
-// block's first row: p lies in the group's own range, so the squares do not cancel however far the mean is from
-// zero.  Blocks are merged by n, mean and M2 = sum (x - mean)^2 (T. F. Chan, G. H. Golub and R. J. LeVeque, "Updating
+// whichever groups they fall in, and sums x - p and its square per channel, p the median of three of the
+// group's values in the block: p lies among them, so the squares do not cancel however far the mean is from zero or one value,
+// channel or row from the others.  Blocks are merged by n, mean and M2 = sum (x - mean)^2 (T. F. Chan, G. H. Golub and R. J. LeVeque, "Updating
 // formulae and a pairwise algorithm for computing sample variances", 1979).
 #pragma once
 #include "gelu.cuh"
@@ -26,8 +29,8 @@ namespace svdq {
 
 enum : int { ACT_NONE = 0, ACT_SILU = 1, ACT_GELU = 2 };
 
-// Threads a block: 640 for large tensors, whose passes are bound by what is in flight (a megapixel of 128 channels: 149
-// us, 161 with 512), 512 for small ones, whose folds and merges are shorter with fewer rows at a time (64 rows of 320:
+// Threads a block: 640 for large tensors, whose passes are bound by what is in flight (a megapixel of 128 channels: 139
+// us, a tenth more with 512), 512 for small ones, whose folds and merges are shorter with fewer rows at a time (64 rows of 320:
 // 6.7 us, 7.1 with 640), and where codes are made (their registers).
 constexpr int GN_MAX_THREADS = 640;
 constexpr int GN_SMALL_THREADS = 512;
@@ -157,6 +160,16 @@ SVDQ_DEV void gn_load(const T* p, int c, uint64_t policy, uint32_t (&w)[Elem<T>:
 // M2 is never negative but for rounding; a NaN stays one.
 SVDQ_DEV float gn_m2(float v) { return v < 0.0f ? 0.0f : v; }
 
+// The pivot of the group of channels first.. in rows lo..hi: the median of its first channel in the first row, its middle
+// one in the middle row and its last one in the last row.
+template <typename T>
+SVDQ_DEV float gn_pivot(const GroupNormArgs& a, const T* X, int lo, int hi, int first, int cg) {
+  const float p = Elem<T>::to_f32(X[(int64_t)lo * a.ldx + first]);
+  const float q = Elem<T>::to_f32(X[(int64_t)((lo + hi) >> 1) * a.ldx + first + (cg >> 1)]);
+  const float r = Elem<T>::to_f32(X[(int64_t)(hi - 1) * a.ldx + first + cg - 1]);
+  return fmaxf(fminf(p, q), fminf(fmaxf(p, q), r));
+}
+
 // (mean, M2) of each group from the n row slots' sums about the pivots, LANES lanes a group.
 template <typename T, int LANES>
 SVDQ_DEV void gn_group_sums(const GroupNormArgs& a, const T* X, int lo, int hi, int n, const float* sum, const float* sq,
@@ -166,7 +179,7 @@ SVDQ_DEV void gn_group_sums(const GroupNormArgs& a, const T* X, int lo, int hi, 
   const float count = (float)(hi - lo) * (float)cg, inv = 1.0f / count;
   for (int g0 = kGroups * (threadIdx.x >> 5); g0 < a.G; g0 += kGroups * (blockDim.x >> 5)) {   // uniform over a warp
     const int g = min(g0 + lane / LANES, a.G - 1);
-    const float pivot = Elem<T>::to_f32(X[(int64_t)lo * a.ldx + g * cg]);
+    const float pivot = gn_pivot(a, X, lo, hi, g * cg, cg);
     float s1 = 0.0f, q1 = 0.0f;
 #pragma unroll 4                                         // 64 loads in flight (2 x 1024 x 1280: 9.0 us, 9.6 without)
     for (int i = g * cg + lane % LANES; i < (g + 1) * cg; i += LANES) {
@@ -199,33 +212,41 @@ SVDQ_DEV void gn_block_stats(const GroupNormArgs& a, const T* X, int lo, int hi,
                              float2* out) {
   constexpr int W = Elem<T>::kWords, U = GN_UNROLL<T, false>;
   const int slot = threadIdx.x / a.nv, v = threadIdx.x - slot * a.nv, c = 8 * v;
-  const int width = 8 * a.nv, cg = a.C / a.G, lane = threadIdx.x & 31;
-  if (slot < a.rp1) {
-    uint32_t x[U][W], nx[U][W];
-    const uint64_t once = l2_policy(false), again = l2_policy(true);
-    const auto fetch = [&](int r0, uint32_t(&x)[U][W]) {
-      const uint64_t policy = r0 >= lo + a.hot ? again : once;
+  const int width = 8 * a.nv, cg = a.C / a.G;
+  uint32_t x[U][W], nx[U][W];
+  const uint64_t once = l2_policy(false), again = l2_policy(true);
+  const auto fetch = [&](int r0, uint32_t(&x)[U][W]) {
+    const uint64_t policy = r0 >= lo + a.hot ? again : once;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (r0 + u * a.rp1 >= hi) continue;
-        const T* row = X + (int64_t)(r0 + u * a.rp1) * a.ldx;
-        if constexpr (LARGE) gn_load<T>(row, c, policy, x[u]);
-        else gn_load<T, VEC>(row, c, a.C, x[u]);
-      }
-    };
-    fetch(lo + slot, x);                                 // in flight together with the pivots
-    float pivot[8], s[8], q[8];
-    int first = c / cg * cg, left = first + cg - c;      // the vector's channels, group by group
+    for (int u = 0; u < U; ++u) {
+      if (r0 + u * a.rp1 >= hi) continue;
+      const T* row = X + (int64_t)(r0 + u * a.rp1) * a.ldx;
+      if constexpr (LARGE) gn_load<T>(row, c, policy, x[u]);
+      else gn_load<T, VEC>(row, c, a.C, x[u]);
+    }
+  };
+  // A thread a group finds the pivots, its loads in flight together with the rows', and hands them round in `sum` (each
+  // thread for its channels: 24 loads, 0.6 us more).
+  float own = 0.0f;
+  if (threadIdx.x < a.G) own = gn_pivot(a, X, lo, hi, threadIdx.x * cg, cg);
+  if (slot < a.rp1) fetch(lo + slot, x);
+  if (threadIdx.x < a.G) sum[threadIdx.x] = own;
+  for (int g = threadIdx.x + blockDim.x; g < a.G; g += blockDim.x) sum[g] = gn_pivot(a, X, lo, hi, g * cg, cg);
+  __syncthreads();
+  float pivot[8], s[8], q[8];
+  if (slot < a.rp1) {
+    int g = c / cg, left = cg * (g + 1) - c;             // the vector's channels, group by group
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      if (left == 0 && c + i < a.C) {
-        first += cg;
-        left = cg;
-      }
-      --left;
-      pivot[i] = Elem<T>::to_f32(X[(int64_t)lo * a.ldx + first]);
+      const bool next = left == 0 && c + i < a.C;
+      g += next ? 1 : 0;
+      left = (next ? cg : left) - 1;
+      pivot[i] = sum[g];
       s[i] = q[i] = 0.0f;
     }
+  }
+  __syncthreads();
+  if (slot < a.rp1) {
     for (int r0 = lo + slot; r0 < hi; r0 += U * a.rp1) {
       fetch(r0 + U * a.rp1, nx);
 #pragma unroll

@@ -181,10 +181,10 @@ SVDQ_DEV uint2 i8_codes(const float (&x)[8], const float (&s)[8], float mul) {
 // of 8 elements of it (vector j at its index + j times the group's size), the same columns in every row, so
 // that their smoothing factors stay in registers; X is read once and held in registers between the maximum
 // and the codes, and the group's next row is on its way while this one is reduced.
-// HBM-bound for many rows (3 K bytes a 16-bit row).  Measured: 18432 x 4096 40.6 us, 0.86 of the copy
-// bandwidth; 4608 x 4096 12.1 us, 0.72 (18.1 with four rows and 512 threads a block, whose registers left one
+// HBM-bound for many rows (3 K bytes a 16-bit row).  Measured: 18432 x 4096 39.1 us, 0.90 of the copy
+// bandwidth; 4608 x 4096 11.7 us, 0.75 (18.1 with four rows and 512 threads a block, whose registers left one
 // block an SM); one row of 4096 1.6 us.  Up to 1024 columns a warp holds a row, without barriers (16384 x
-// 320: 5.3 us, 5.8 with a block a row), unless the rows are too few to fill the GPU with warps (77 x 640: 1.9 us,
+// 320: 5.2 us, 5.8 with a block a row), unless the rows are too few to fill the GPU with warps (77 x 640: 1.9 us,
 // 1.5 with a block); up to 16384 a block does; beyond that k_quantize_long_i8 reads rows twice.
 constexpr int QI_MAX_THREADS = 512;
 template <typename T, int VPT, bool WARP>

@@ -51,6 +51,11 @@ SVDQ_DEV void store_y(void* Y, int type, int64_t at, float y) {
 // its 128 tokens in TMEM twice over (columns 0 and 256), so that a tile's epilogue runs under the next
 // tile's MMAs.  A pair's MMA reads each operand byte from shared memory half as often as two CTAs' own
 // would, and each CTA copies half of B.
+// Bound by the tensor pipe, and in long runs by the power limit: 4608 x 4096 of K = 12288 138 us (3.36 POP/s), 4608 x
+// 12288 of K = 4096 143, 4096 cubed 47.6; the pipe is busy 82 % of the active cycles at 4608 x 4096 of K = 4096.  Narrow
+// outputs are bound by the stores and by the last wave: 16384 x 320 of K = 320 8.6 us, 8192 x 1280 of K = 1280 16.7 (steps
+// of 64 in nt: 9.2 and 18.4).  Roles are walked by whole warps that elect a lane for each copy and MMA: with one lane in a
+// divergent branch a ring slot took 600 cycles to issue.
 //   warp 0      copies: A and B boxes, both CTAs counting on the leader's barrier
 //   warp 1      leader only: MMAs;  in both: TMEM
 //   warps 4-11  epilogue: TMEM -> registers, scales and bias, stores (two warps a lane quarter)
@@ -66,9 +71,7 @@ constexpr int LP_OFF_BAR = LP_OFF_STG + LP_EPI_WARPS * LP_STG_BYTES;
 constexpr int LP_SMEM = LP_OFF_BAR + 256 + 1024;
 static_assert(LP_SMEM <= 232448, "shared memory of a CTA");
 
-#ifndef LP_RASTER
-#define LP_RASTER 8
-#endif
+constexpr int LP_RASTER = 8;                             // 4, 12 and 16 measured no better
 // Tiles run in groups of LP_RASTER row blocks, the row block fastest: the pairs at work at one time
 // share few rows of X and few of Wq, which stay in L2.
 SVDQ_DEV void pair_tile(int t, int num_m, int num_n, int& mb, int& nb) {
@@ -332,7 +335,9 @@ __global__ void __launch_bounds__(LP_THREADS, 1) k_linear_i8_pair(
 // full whatever N is.  Each CTA streams its K range through a ring, leaves its integer sums in shared
 // memory, and after a cluster barrier sums a share of the tile's outputs over the cluster's CTAs (integers:
 // the order does not matter).
-//   warp 0  copies, warp 1 MMAs and TMEM;  then all eight warps the epilogue
+// Bound by the weight's bytes where it is large (1 x 12288 of K = 4096 11.4 us, 50 MB: 0.68 of the copy bandwidth, 3.5 us
+// of it launch, first loads and reduction), else by those latencies (1 x 4096 of K = 4096 from L2 4.8 us).
+//   warp 0  copies, warp 1 MMAs and TMEM;  then all warps the epilogue
 // TMEM: CTAs of several such kernels may share an SM, and one that waits for columns while its cluster waits for it
 // must not meet another in the same position.  With a cluster a CTA has at least two ring slots, so at most six (nt
 // 16..32: 32 columns each), four (33..80: 64 or 128) or three (81..128: 128) fit an SM's shared memory: 512 columns always do.
