@@ -284,3 +284,27 @@ def test_the_same_call_gives_the_same_bits():
     X, gamma, beta = _case(2, 3000, 320, "fp32", 41)
     Y = _run(X, 2, 3000, 320, 32, gamma, beta, 1e-5, "silu")
     assert all(torch.equal(Y, _run(X, 2, 3000, 320, 32, gamma, beta, 1e-5, "silu")) for _ in range(10))
+
+
+@pytest.mark.parametrize("B,S,C", [(1, 64, 320), (1, 4096, 320), (2, 700, 637), (160, 300, 64)])
+def test_norms_in_place_one_after_another(B, S, C):
+    """Launch after launch on the same memory: each reads what the one before it wrote, whichever block that was."""
+    L = _lib()
+    G = 7 if C == 637 else 32
+    g = torch.Generator(device="cuda").manual_seed(8)
+    X0 = torch.randn(B, S, C, device="cuda", generator=g).to(torch.bfloat16)
+    gamma = [torch.rand(C, device="cuda", generator=g) + 0.5 for _ in range(3)]
+    X = X0.clone()
+    ws = L.new_group_norm_workspace(B, S, C, G)
+
+    def run(sync):
+        X.copy_(X0)
+        for i in range(12):
+            L.svdq_group_norm(X, B, S, C, G, gamma[i % 3], None, 1e-5, L.SVDQ_ACT_SILU, X, ws)
+            if sync:
+                torch.cuda.synchronize()
+        return X.clone()
+
+    want = run(True)
+    for _ in range(20):
+        assert torch.equal(run(False), want)

@@ -375,3 +375,36 @@ def test_rows_that_graphs_and_neighbours_share_with_few_tokens():
         G.replay()
         assert torch.equal(bufs[-1], want)
         assert torch.equal(chain(False), want)
+
+
+@pytest.mark.parametrize("M", [1, 4, 40, 600])
+def test_two_buffers_passed_to_and_fro(M):
+    """Layers that write one another's input, launch after launch: each reads what the launch just before it wrote where
+    earlier ones had read and written other values."""
+    C = _lib()
+    K = 1024
+    g = torch.Generator(device="cuda").manual_seed(7)
+    W = [torch.randint(-127, 128, (K, K), device="cuda", generator=g, dtype=torch.int8) for _ in range(3)]
+    sw = torch.full((K,), 1.0 / (73.0 * 32.0), device="cuda")
+    ws = torch.empty(C.svdq_forward_i8_workspace_bytes(M, K), dtype=torch.uint8, device="cuda")
+    X = torch.randn(M, K, device="cuda", generator=g).to(torch.bfloat16)
+    pair = [X.clone(), torch.empty_like(X)]
+
+    def run(sync):
+        pair[0].copy_(X)
+        for i in range(24):
+            C.svdq_forward_i8(pair[i % 2], M, K, None, W[i % 3], sw, None, pair[(i + 1) % 2], K, ws)
+            if sync:
+                torch.cuda.synchronize()
+        return pair[0].clone()
+
+    want = run(True)
+    assert bool(want.isfinite().all()) and float(want.abs().max()) > 0
+    for _ in range(20):
+        assert torch.equal(run(False), want)
+    G = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(G):
+        run(False)
+    for _ in range(20):
+        G.replay()
+        assert torch.equal(pair[0], want)

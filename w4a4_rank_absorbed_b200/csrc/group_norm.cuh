@@ -11,15 +11,15 @@
 //                  Each block of the first leaves (mean, M2) of its rows per group, each block of the second
 //                  merges those of its sample: nothing needs clearing, no block waits for another.
 // The order of every sum is fixed.
-// Measured: a megapixel of 128 bf16 channels with SiLU 139 us, 0.8 GB moved, 0.90 of the copy bandwidth; 2 x 4096 x 640
-// 11.2 us (9.7 without SiLU; two launches' latencies are 6 of it); 64 x 320 6.7 us (one launch).  Codes: 2 x 1024 x 1280
-// 10.6 us, 16384 x 320 15.6 us (issue-bound: of a row's 64 threads 40 hold a vector).
+// Measured: a megapixel of 128 bf16 channels with SiLU 139 us, 0.83 of the copy bandwidth (0.8 GB, 64 MB of it
+// from L2); 2 x 4096 x 640 11.2 us (9.7 without SiLU; two launches' latencies are 6 of it); 64 x 320 6.7 us (one
+// launch).  Codes: 2 x 1024 x 1280 10.6 us, 16384 x 320 15.6 us (issue-bound: of a row's 64 threads 40 hold a vector).
 //
 // Statistics: a thread owns 8 consecutive channels (a 16-byte vector of a 16-bit type) of every rp-th row,
 // whichever groups they fall in, and sums x - p and its square per channel, p the median of three of the
-// group's values in the block: p lies among them, so the squares do not cancel however far the mean is from zero or one value,
-// channel or row from the others.  Blocks are merged by n, mean and M2 = sum (x - mean)^2 (T. F. Chan, G. H. Golub and R. J. LeVeque, "Updating
-// formulae and a pairwise algorithm for computing sample variances", 1979).
+// group's values in the block: p lies among them, so the squares do not cancel however far the mean is from zero or
+// one value, channel or row from the others.  Blocks are merged by n, mean and M2 = sum (x - mean)^2 (T. F. Chan, G.
+// H. Golub and R. J. LeVeque, "Updating formulae and a pairwise algorithm for computing sample variances", 1979).
 #pragma once
 #include "gelu.cuh"
 #include "int8.cuh"
@@ -30,8 +30,8 @@ namespace svdq {
 enum : int { ACT_NONE = 0, ACT_SILU = 1, ACT_GELU = 2 };
 
 // Threads a block: 640 for large tensors, whose passes are bound by what is in flight (a megapixel of 128 channels: 139
-// us, a tenth more with 512), 512 for small ones, whose folds and merges are shorter with fewer rows at a time (64 rows of 320:
-// 6.7 us, 7.1 with 640), and where codes are made (their registers).
+// us, 8 % more with 512), 512 for small ones, whose folds and merges are shorter with fewer rows at a time (64 rows
+// of 320: 6.7 us, 7.1 with 640), and where codes are made (their registers).
 constexpr int GN_MAX_THREADS = 640;
 constexpr int GN_SMALL_THREADS = 512;
 constexpr int GN_MAX_C = 8 * GN_SMALL_THREADS;
@@ -160,8 +160,8 @@ SVDQ_DEV void gn_load(const T* p, int c, uint64_t policy, uint32_t (&w)[Elem<T>:
 // M2 is never negative but for rounding; a NaN stays one.
 SVDQ_DEV float gn_m2(float v) { return v < 0.0f ? 0.0f : v; }
 
-// The pivot of the group of channels first.. in rows lo..hi: the median of its first channel in the first row, its middle
-// one in the middle row and its last one in the last row.
+// The pivot of the group of channels first.. in rows lo..hi: the median of its first channel in the first row, its
+// middle one in the middle row and its last one in the last row.
 template <typename T>
 SVDQ_DEV float gn_pivot(const GroupNormArgs& a, const T* X, int lo, int hi, int first, int cg) {
   const float p = Elem<T>::to_f32(X[(int64_t)lo * a.ldx + first]);
@@ -388,9 +388,9 @@ struct GnApply {
 
 // Second pass over rows lo..hi of sample b, from the last to the first (t.fetch has the first step's rows).  stat:
 // (mean, rstd) of the groups; KEEP: the rows are in `kept`.  QUANT: instead of Y, rows of 8-bit codes and their
-// scales.  A row's l2 threads are whole warps, or 4 to 32 lanes of one, a power of two: its maximum is a reduction over lanes, and
-// over warps through `top` (two buffers of U words a warp; one barrier of the row's warps a step: l2 >= 64 there, so at
-// most 8 rows and barriers).
+// scales.  A row's l2 threads are whole warps, or 4 to 32 lanes of one, a power of two: its maximum is a reduction
+// over lanes, and over warps through `top` (two buffers of U words a warp; one barrier of the row's warps a step: l2
+// >= 64 there, so at most 8 rows and barriers).
 template <typename T, bool VEC, bool QUANT, bool KEEP, int ACT>
 SVDQ_DEV void gn_apply_loop(const GroupNormArgs& a, GnApply<T, VEC, QUANT, KEEP>& t, const T* X, int b, int lo, int hi,
                             const float2 (&mu)[4], const float2 (&ga)[4], const float2 (&be)[4], const uint4* kept,
@@ -475,8 +475,8 @@ SVDQ_DEV void gn_apply_loop(const GroupNormArgs& a, GnApply<T, VEC, QUANT, KEEP>
 #pragma unroll
         for (int u = 0; u < U; ++u)
           if (lane == u) now[u * (blockDim.x >> 5) + warp] = m[u];
-        // Only the warps of this row wait for one another, so that the rows' chains of latencies overlap (a row's threads
-        // are whole warps; warps past the last row take no part).
+        // Only the warps of this row wait for one another, so that the rows' chains of latencies overlap (a row's
+        // threads are whole warps; warps past the last row take no part).
         if (slot < a.rp2) {
           asm volatile("bar.sync %0, %1;" ::"r"(1 + slot), "r"(a.l2) : "memory");
 #pragma unroll

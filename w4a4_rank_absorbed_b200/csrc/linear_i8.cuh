@@ -46,16 +46,16 @@ SVDQ_DEV void store_y(void* Y, int type, int64_t at, float y) {
 }
 
 // ------------------------------------------------------------------ pair kernel ---
-// Many tokens: persistent CTA pairs (one CTA an SM), tiles of 256 tokens x nt channels (nt a multiple of 32, 64..256), each
-// CTA holding 128 of the tokens and half of the channels' codes in a 6-slot ring of 32 KB, and the sums of
-// its 128 tokens in TMEM twice over (columns 0 and 256), so that a tile's epilogue runs under the next
-// tile's MMAs.  A pair's MMA reads each operand byte from shared memory half as often as two CTAs' own
-// would, and each CTA copies half of B.
+// Many tokens: persistent CTA pairs (one CTA an SM), tiles of 256 tokens x nt channels (nt a multiple of 32,
+// 64..256), each CTA holding 128 of the tokens and half of the channels' codes in a 6-slot ring of 32 KB, and the
+// sums of its 128 tokens in TMEM twice over (columns 0 and 256), so that a tile's epilogue runs under the next tile's
+// MMAs.  A pair's MMA reads each operand byte from shared memory half as often as two CTAs' own would, and each CTA
+// copies half of B.
 // Bound by the tensor pipe, and in long runs by the power limit: 4608 x 4096 of K = 12288 138 us (3.36 POP/s), 4608 x
-// 12288 of K = 4096 143, 4096 cubed 47.6; the pipe is busy 82 % of the active cycles at 4608 x 4096 of K = 4096.  Narrow
-// outputs are bound by the stores and by the last wave: 16384 x 320 of K = 320 8.6 us, 8192 x 1280 of K = 1280 16.7 (steps
-// of 64 in nt: 9.2 and 18.4).  Roles are walked by whole warps that elect a lane for each copy and MMA: with one lane in a
-// divergent branch a ring slot took 600 cycles to issue.
+// 12288 of K = 4096 143, 4096 cubed 47.6; the pipe is busy 82 % of the active cycles at 4608 x 4096 of K = 4096.
+// Narrow outputs are bound by the stores and by the last wave: 16384 x 320 of K = 320 8.6 us, 8192 x 1280 of K = 1280
+// 16.7 (steps of 64 in nt: 9.2 and 18.4).  Roles are walked by whole warps that elect a lane for each copy and MMA:
+// with one lane in a divergent branch a ring slot took 600 cycles to issue.
 //   warp 0      copies: A and B boxes, both CTAs counting on the leader's barrier
 //   warp 1      leader only: MMAs;  in both: TMEM
 //   warps 4-11  epilogue: TMEM -> registers, scales and bias, stores (two warps a lane quarter)
@@ -335,19 +335,21 @@ __global__ void __launch_bounds__(LP_THREADS, 1) k_linear_i8_pair(
 // full whatever N is.  Each CTA streams its K range through a ring, leaves its integer sums in shared
 // memory, and after a cluster barrier sums a share of the tile's outputs over the cluster's CTAs (integers:
 // the order does not matter).
-// Bound by the weight's bytes where it is large (1 x 12288 of K = 4096 11.4 us, 50 MB: 0.68 of the copy bandwidth, 3.5 us
-// of it launch, first loads and reduction), else by those latencies (1 x 4096 of K = 4096 from L2 4.8 us).
+// Bound by the weight's bytes where it is large (1 x 12288 of K = 4096 11.4 us, 50 MB: 0.68 of the copy bandwidth,
+// 3.5 us of it launch, first loads and reduction), else by those latencies (1 x 4096 of K = 4096 from L2 4.8 us).
 //   warp 0  copies, warp 1 MMAs and TMEM;  then all warps the epilogue
 // TMEM: CTAs of several such kernels may share an SM, and one that waits for columns while its cluster waits for it
 // must not meet another in the same position.  With a cluster a CTA has at least two ring slots, so at most six (nt
-// 16..32: 32 columns each), four (33..80: 64 or 128) or three (81..128: 128) fit an SM's shared memory: 512 columns always do.
+// 16..32: 32 columns each), four (33..80: 64 or 128) or three (81..128: 128) fit an SM's shared memory: 512 columns
+// always do.
 constexpr int LS_THREADS = 256;
 constexpr int LS_A_BYTES = 128 * 128;
 constexpr int LS_TAIL_BYTES = 256 + 1024;                 // barriers, then the tile's token scales
 
 // One or a few tokens quantized by the GEMM itself (XT their type; int8_t: they come as codes): every CTA reads
-// all of their rows for the maxima (L2 holds them, and a cluster barrier to share them would cost more), then writes the codes of its
-// own K range where TMA would have put them, while the first weight boxes are on their way.  One launch instead of two.
+// all of their rows for the maxima (from L2; sharing the maxima would take a cluster barrier), then writes
+// the codes of its own K range where TMA would have put them, while the first weight boxes are on their way.  One
+// launch instead of two.
 constexpr int LS_FUSED_TOKENS = 16;                       // nt; a chunk of 128 of K is 16 rows of 128 bytes
 constexpr int LS_FUSED_CHUNK = LS_FUSED_TOKENS * 128;
 constexpr int LS_FUSED_THREADS = 512;
@@ -356,8 +358,8 @@ __host__ __device__ constexpr int split_threads() {
   return std::is_same<XT, int8_t>::value ? LS_THREADS : LS_FUSED_THREADS;
 }
 // All threads.  A half warp takes one of the rows' chunks of 128 columns, whose x_hat stays in registers between the
-// maximum and the codes (with two or four chunks a half warp, code that runs once and is not in the instruction cache yet
-// cost 0.2 and 0.6 us).  top: zeroes; codes: the CTA's chunks, k_lo to k_hi.
+// maximum and the codes (with two or four, unrolled, the longer code alone cost 0.2 and 0.6 us where it had
+// nothing to do).  top: zeroes; codes: the CTA's chunks, k_lo to k_hi.
 template <typename T>
 SVDQ_DEV void quantize_tokens(const LinearI8Args& a, int k_lo, int k_hi, uint32_t* top, float* sxs, uint8_t* codes) {
   const int nkt = (a.K + 127) >> 7, l = threadIdx.x & 15;

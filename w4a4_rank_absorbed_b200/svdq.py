@@ -456,6 +456,8 @@ def _cuda_index(t, name: str) -> int:
 # torch's current stream as a raw handle, without the Stream object around it (where this torch has it)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+# and its current device without the check that CUDA is up (a CUDA tensor has shown that)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _on(stream, dev: int, where: str) -> int:
@@ -479,7 +481,7 @@ class _Entry:
     def __call__(self, dev: int, stream, *args) -> None:
         block = self.pack(*args, _on(stream, dev, self.name))
         call = (_lib or load_library()).svdq_call
-        if torch.cuda.current_device() == dev:
+        if _raw_device() == dev:
             st = call(self.index, block)
         else:
             with torch.cuda.device(dev):
