@@ -408,3 +408,23 @@ def test_two_buffers_passed_to_and_fro(M):
     for _ in range(20):
         G.replay()
         assert torch.equal(pair[0], want)
+
+
+@pytest.mark.parametrize("M,N,K", [(12964, 390, 1552), (19264, 256, 1072), (12729, 270, 1856), (6169, 494, 1696),
+                                   (16384, 1280, 1280), (18999, 1001, 272)])
+def test_last_rounds_in_strips(M, N, K):
+    """Many tiles with few left for the last round.  Every step is exact or one rounding of binary32, so results are bits:
+    the sums are whole numbers below 2^53, and the product of two float32 numbers is exact in float64."""
+    C = _lib()
+    g = torch.Generator(device="cuda").manual_seed(M)
+    q = torch.randint(-127, 128, (M, K), device="cuda", generator=g, dtype=torch.int8)
+    W = torch.randint(-127, 128, (N, K), device="cuda", generator=g, dtype=torch.int8)
+    sx, sw = torch.rand(M, device="cuda", generator=g), torch.rand(N, device="cuda", generator=g)
+    full = torch.full((M, N + 8), 7.0, device="cuda")
+    C.svdq_linear_i8(q, sx, W, sw, None, full[:, :N], M, N, K)
+    torch.cuda.synchronize()
+    assert C.svdq_get_device_error() == (0, 0)
+    acc = (q.double() @ W.double().T).float()
+    want = ((acc * sx[:, None]).double() * sw.double()[None, :]).float()
+    assert torch.equal(full[:, :N], want)
+    assert bool((full[:, N:] == 7.0).all())

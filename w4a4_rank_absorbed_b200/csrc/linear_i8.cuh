@@ -24,6 +24,7 @@ struct LinearI8Args {
   int64_t ldy;
   int M, N, K;
   int nt;               // columns (pair kernel) or tokens (split kernel) of a tile
+  int cut, strips;      // pair kernel: tiles from `cut` on are taken in `strips` strips of columns each
   int stages;           // ring slots (split kernel)
   int w_early;          // split kernel: the weight may be read before griddepcontrol.wait
   const void* X;        // split kernel that quantizes its tokens itself: their rows and smoothing factors
@@ -52,7 +53,7 @@ SVDQ_DEV void store_y(void* Y, int type, int64_t at, float y) {
 // MMAs.  A pair's MMA reads each operand byte from shared memory half as often as two CTAs' own would, and each CTA
 // copies half of B.
 // Bound by the tensor pipe, and in long runs by the power limit: 4608 x 4096 of K = 12288 138 us (3.36 POP/s), 4608 x
-// 12288 of K = 4096 143, 4096 cubed 47.6; the pipe is busy 82 % of the active cycles at 4608 x 4096 of K = 4096.
+// 12288 of K = 4096 143, 4096 cubed 46.3; the pipe is busy 82 % of the active cycles at 4608 x 4096 of K = 4096.
 // Narrow outputs are bound by the stores and by the last wave: 16384 x 320 of K = 320 8.6 us, 8192 x 1280 of K = 1280
 // 16.7 (steps of 64 in nt: 9.2 and 18.4).  Roles are walked by whole warps that elect a lane for each copy and MMA:
 // with one lane in a divergent branch a ring slot took 600 cycles to issue.
@@ -81,6 +82,22 @@ SVDQ_DEV void pair_tile(int t, int num_m, int num_n, int& mb, int& nb) {
   const int w = t % per_group;
   mb = first + w % gm;
   nb = w / gm;
+}
+
+// What a pair does at a time: columns col.. (w of them) of row block mb.  The tiles before a.cut fill whole rounds of
+// all pairs; the last round's, where they are few, come in strips, so that more pairs share them.
+struct PairWork {
+  int mb, col, w;
+};
+SVDQ_DEV PairWork pair_work(const LinearI8Args& a, int i, int num_m, int num_n) {
+  const bool whole = i < a.cut;
+  const int tile = whole ? i : a.cut + (i - a.cut) / a.strips;
+  PairWork p;
+  int nb;
+  pair_tile(tile, num_m, num_n, p.mb, nb);
+  p.w = whole ? a.nt : a.nt / a.strips;
+  p.col = nb * a.nt + (whole ? 0 : (i - a.cut) % a.strips * p.w);
+  return p;
 }
 
 // 32 columns from n0 of one row a lane: rows row0 + lane (below a.M), sums v.  chan: the columns' scales, and
@@ -148,6 +165,7 @@ SVDQ_DEV void store_chunk(const LinearI8Args& a, const uint32_t (&v)[32], int ro
 __global__ void __launch_bounds__(LP_THREADS, 1) k_linear_i8_pair(
     const __grid_constant__ CUtensorMap tm_x,    // uint8 {K, M}, box {128, 128}, SW128
     const __grid_constant__ CUtensorMap tm_w,    // uint8 {K, N}, box {128, nt / 2}, SW128
+    const __grid_constant__ CUtensorMap tm_s,    // the same with box {128, nt / strips / 2}
     const LinearI8Args a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -163,7 +181,7 @@ __global__ void __launch_bounds__(LP_THREADS, 1) k_linear_i8_pair(
   const uint32_t rank = warp_uniform(cluster_rank());
   const int nkt = (a.K + 127) >> 7;
   const int num_m = (a.M + 255) >> 8, num_n = (a.N + a.nt - 1) / a.nt;
-  const int total = num_m * num_n, first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  const int total = a.cut + (num_m * num_n - a.cut) * a.strips, first = blockIdx.x >> 1, step = gridDim.x >> 1;
   const uint64_t tmo = L8_TIMEOUT_NS;
 
   if (threadIdx.x == 0) {
@@ -196,14 +214,14 @@ __global__ void __launch_bounds__(LP_THREADS, 1) k_linear_i8_pair(
 
   if (warp == 0) {
     // ------------------------------------------------------------------ copies ---
-    const uint32_t bytes = 2 * (LP_A_BYTES + (uint32_t)(a.nt / 2) * 128u);   // of both CTAs
     int s = 0, issued = 0;
     uint32_t phase = 1;
     bool ok = true;
     for (int t = first; t < total && ok; t += step) {
-      int mb, nb;
-      pair_tile(t, num_m, num_n, mb, nb);
-      const int ya = mb * 256 + (int)rank * 128, yb = nb * a.nt + (int)rank * (a.nt / 2);
+      const PairWork p = pair_work(a, t, num_m, num_n);
+      const int ya = p.mb * 256 + (int)rank * 128, yb = p.col + (int)rank * (p.w / 2);
+      const uint32_t bytes = 2 * (LP_A_BYTES + (uint32_t)(p.w / 2) * 128u);    // of both CTAs
+      const CUtensorMap* tm_b = t < a.cut ? &tm_w : &tm_s;
       for (int kt = 0; kt < nkt; ++kt) {
         if (!mbar_wait_warp(&empty[s], phase, tmo, abort_flag, 0x501)) {
           ok = false;
@@ -215,7 +233,7 @@ __global__ void __launch_bounds__(LP_THREADS, 1) k_linear_i8_pair(
           if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
           if (SVDQ_CHECK_OK(ya >= 0 && yb >= 0 && (uint32_t)(dst - smem_raw) + LP_STAGE_BYTES <= dyn_smem_bytes(), 0x5c1)) {
             tma_load_2d_pair(dst, &tm_x, bar, kt * 128, ya);
-            tma_load_2d_pair(dst + LP_A_BYTES, &tm_w, bar, kt * 128, yb);
+            tma_load_2d_pair(dst + LP_A_BYTES, tm_b, bar, kt * 128, yb);
           }
         }
         __syncwarp();
@@ -234,12 +252,12 @@ __global__ void __launch_bounds__(LP_THREADS, 1) k_linear_i8_pair(
     }
   } else if (warp == 1 && rank == 0) {
     // -------------------------------------------------------------------- MMAs ---
-    const uint32_t idesc = idesc_i8(256, a.nt);
     const uint64_t desc0 = sdesc_kmajor_sw128(smem_u32(smem));
     int s = 0, n = 0;
     uint32_t phase = 0;
     bool ok = true;
     for (int t = first; t < total && ok; t += step, ++n) {
+      const uint32_t idesc = idesc_i8(256, t < a.cut ? a.nt : a.nt / a.strips);
       const uint32_t d = tbase + 256u * (uint32_t)(n & 1);
       if (n >= 2 && !mbar_wait_warp(&acc_empty[n & 1], (uint32_t)(((n >> 1) - 1) & 1), tmo, abort_flag, 0x511)) break;
       tc_fence_after();
@@ -274,12 +292,11 @@ __global__ void __launch_bounds__(LP_THREADS, 1) k_linear_i8_pair(
     const int ew = warp - LP_EPI_WARP0, q = warp & 3, h = ew >> 2;
     float* stg = reinterpret_cast<float*>(smem + LP_OFF_STG + ew * LP_STG_BYTES);
     float* chan = stg + 512;
-    const int last = (((a.nt >> 5) - 1 - h) & ~1) + h;   // this warp's 32-column chunks: h, h + 2, .. last
     int n = 0;
     for (int t = first; t < total; t += step, ++n) {
-      int mb, nb;
-      pair_tile(t, num_m, num_n, mb, nb);
-      const int row0 = mb * 256 + (int)rank * 128 + 32 * q, col0 = nb * a.nt + 32 * h;
+      const PairWork p = pair_work(a, t, num_m, num_n);
+      const int last = (((p.w >> 5) - 1 - h) & ~1) + h;  // this warp's 32-column chunks: h, h + 2, .. last
+      const int row0 = p.mb * 256 + (int)rank * 128 + 32 * q, col0 = p.col + 32 * h;
       const float sx = row0 + lane < a.M ? __ldg(a.sx + row0 + lane) : 0.0f;
       __syncwarp();                                      // the last tile's reads of them are done
       // the tile's channel scales and biases, while the sums are on their way
@@ -316,7 +333,7 @@ __global__ void __launch_bounds__(LP_THREADS, 1) k_linear_i8_pair(
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&acc_empty[n & 1]), 0));
         }
-        store_chunk(a, v, row0, nb * a.nt + 32 * c, sx, smem_u32(chan) + 64u * (uint32_t)(c - h), stg);
+        store_chunk(a, v, row0, p.col + 32 * c, sx, smem_u32(chan) + 64u * (uint32_t)(c - h), stg);
       }
     }
   }

@@ -541,22 +541,32 @@ std::atomic<bool> g_pair_attr[kMaxDevices], g_split_attr[kMaxDevices];
 // Splits of 5 and 7 are left out: clusters of that size leave SMs of a GPC idle.
 // (measured, both sides: 512 x 320 of K = 320: split nt 16 3.5 us, pair nt 64 4.1; 128 x 4096 of K = 4096: split
 // nt 64, s 2 7.9, pair nt 64 9.0; 256 x 4096 of K = 4096: pair nt 64 8.9, split nt 64, s 2 10.7.)
+// strips: in how many strips of columns the tiles of the pair kernel's last round are taken, where they are few: main and
+// the last terms are then those of nt / strips, and 1 more (measured: 16384 x 1280 of K = 1280 26.5 us with two strips,
+// 28.4 with whole tiles of the best width; 4096 x 4096 of K = 4096 46.5 and 48.1; 5120 x 4000 of K = 2048, where whole
+// tiles are foreseen 0.4 slower, 32.1 and 31.4).
 struct LinearI8Plan {
   bool pair;
-  int nt, split;
+  int nt, split, strips;
 };
 LinearI8Plan find_plan_linear_i8(int64_t M, int64_t N, int64_t K, int sms) {
   const int64_t nkt = (K + 127) / 128;
-  LinearI8Plan best = {true, 256, 1};
+  LinearI8Plan best = {true, 256, 1, 1};
   double least = 1e30;
   const auto waves = [](int64_t tiles, int64_t at_once) { return (double)((tiles + at_once - 1) / at_once); };
   for (int nt = 256; nt >= 64; nt -= 32) {
     const int64_t tiles = (M + 255) / 256 * ((N + nt - 1) / nt);
-    const double main = (double)nkt * (0.11 + 0.001 * nt);
-    const double t = 2.6 + main + (waves(tiles, sms / 2) - 1) * std::max(main, 1.65 + 0.0068 * nt) + 0.3 + 0.0095 * nt;
-    if (t < least) {
-      least = t;
-      best = {true, nt, 1};
+    const double main = (double)nkt * (0.11 + 0.001 * nt), rest = 1.65 + 0.0068 * nt, w = waves(tiles, sms / 2);
+    for (const int q : {1, 2, 4}) {
+      const int64_t few = tiles % (sms / 2);
+      if (q > 1 && (tiles < sms / 2 || few == 0 || few * q > sms / 2 || nt % (32 * q) != 0 || nt / q < 64)) continue;
+      const double last = (double)nkt * (0.11 + 0.001 * (nt / q));
+      const double t = 2.6 + (w - 1) * std::max(main, rest) + (q == 1 ? main : std::max(last, rest) + 1.0) + 0.3 +
+                       0.0095 * (nt / q);
+      if (t < least) {
+        least = t;
+        best = {true, nt, 1, q};
+      }
     }
   }
   const int m16 = (int)std::min<int64_t>((M + 15) / 16 * 16, 128);   // all the tokens, where they fit a tile
@@ -571,7 +581,7 @@ LinearI8Plan find_plan_linear_i8(int64_t M, int64_t N, int64_t K, int sms) {
                                                 tok * (0.008 + 0.022 / s));
       if (t < least) {
         least = t;
-        best = {false, tok, s};
+        best = {false, tok, s, 1};
       }
     }
     if (nt >= m16) break;
@@ -666,8 +676,15 @@ svdq_status launch_linear_i8(int dev, DevInfo* d, const int8_t* Xq, const float*
     const int64_t tiles = (M + 255) / 256 * ((N + p.nt - 1) / p.nt);
     if (tiles > kMaxDim) return SVDQ_ERR_UNSUPPORTED_SHAPE;
     if ((st = allow_smem(k_linear_i8_pair, dev, g_pair_attr, LP_SMEM)) != SVDQ_OK) return st;
-    if (launch_pdl(k_linear_i8_pair, dim3((unsigned)(2 * std::min<int64_t>(tiles, d->sms / 2))), dim3(LP_THREADS),
-                   (size_t)LP_SMEM, s, 2, tm_x, tm_w, a) != cudaSuccess)
+    const int64_t pairs = std::min<int64_t>(tiles, d->sms / 2);
+    a.strips = p.strips;
+    a.cut = (int)(p.strips > 1 ? tiles / pairs * pairs : tiles);
+    CUtensorMap tm_s = tm_w;
+    if (p.strips > 1 && !make_map_2d(&tm_s, CU_TENSOR_MAP_DATA_TYPE_UINT8, Wq, (uint64_t)K, (uint64_t)N, (uint64_t)K, 128,
+                                     (uint32_t)(p.nt / p.strips / 2)))
+      return SVDQ_ERR_CUDA;
+    if (launch_pdl(k_linear_i8_pair, dim3((unsigned)(2 * pairs)), dim3(LP_THREADS), (size_t)LP_SMEM, s, 2, tm_x, tm_w,
+                   tm_s, a) != cudaSuccess)
       return launch_failed();
     return launch_status();
   }
