@@ -399,6 +399,7 @@ SVDQ_API svdq_status svdq_linear_i8(const int8_t* Xq, const float* sx, const int
  * svdq_forward_i8 -- the layer in one call: svdq_quantize_act_i8 into the
  * workspace, then svdq_linear_i8 (one launch that does both where M ceil(K / 128)
  * <= 32: one token of up to 4096 columns); the same results as the two calls.
+ * Y may lie on X's memory.
  *   workspace [scratch] svdq_forward_i8_workspace_bytes(M, K) bytes, no initial
  *             contents needed; calls that may overlap need workspaces of their own.
  */

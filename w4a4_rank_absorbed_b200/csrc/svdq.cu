@@ -615,7 +615,7 @@ bool fuse_tokens_i8(const LinearI8Plan& p, int64_t M, int64_t K) {
   return !p.pair && M <= LS_FUSED_TOKENS && M * ((K + 127) / 128) <= LS_FUSED_THREADS / 16;
 }
 
-// Whether [a, a + rows) and [b, b + rows) may share bytes.
+// Whether na bytes from a and nb bytes from b share any.
 bool may_overlap(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + nb && y < x + na;
